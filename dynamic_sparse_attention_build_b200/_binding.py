@@ -34,7 +34,8 @@ KIND_CODES = {"ashape": DSA_KIND_ASHAPE, "vs": DSA_KIND_VS, "block_topk": DSA_KI
 
 EXPORTS = ("dsa_workspace_size", "dsa_build_indices", "dsa_sparse_prefill", "dsa_count_pairs",
            "dsa_get_device_status", "dsa_selftest_wait_timeout", "dsa_status_string",
-           "dsa_last_cuda_error", "dsa_build_indices_static", "dsa_set_wait_limit")
+           "dsa_last_cuda_error", "dsa_build_indices_static", "dsa_set_wait_limit",
+           "dsa_packed_prefill")
 
 
 class dsa_problem(ctypes.Structure):
@@ -97,6 +98,9 @@ def lib():
         L.dsa_get_device_status.argtypes = [ctypes.c_void_p, P(ctypes.c_int32)]
         L.dsa_selftest_wait_timeout.argtypes = [ctypes.c_uint32, ctypes.c_void_p]
         L.dsa_set_wait_limit.argtypes = [ctypes.c_uint64]
+        L.dsa_packed_prefill.argtypes = [P(dsa_problem), ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p,
+                                         ctypes.c_void_p, ctypes.c_int32, ctypes.c_void_p, ctypes.c_void_p,
+                                         ctypes.c_void_p]
         L.dsa_status_string.argtypes = [ctypes.c_int]
         L.dsa_status_string.restype = ctypes.c_char_p
         L.dsa_last_cuda_error.argtypes = []
@@ -145,6 +149,11 @@ def dsa_sparse_prefill(problem, Q_ptr, K_ptr, V_ptr, indices, O_ptr, lse_ptr, st
 
 def dsa_count_pairs(problem, indices, pairs_ptr, stream_ptr):
     return lib().dsa_count_pairs(ctypes.byref(problem), ctypes.byref(indices), pairs_ptr, stream_ptr)
+
+
+def dsa_packed_prefill(problem, Q_ptr, K_ptr, V_ptr, cu_ptr, n_seq, O_ptr, lse_ptr, stream_ptr):
+    return lib().dsa_packed_prefill(ctypes.byref(problem), Q_ptr, K_ptr, V_ptr, cu_ptr, n_seq, O_ptr, lse_ptr,
+                                    stream_ptr)
 
 
 def dsa_get_device_status(stream_ptr):

@@ -33,7 +33,8 @@
  *   - Errors a kernel finds (an index list longer than its capacity, an index out
  *     of range, a malformed list, a bounded wait that ran out) are recorded in the
  *     status word of the call's stream and reported by dsa_get_device_status.
- *   - Batch size is one sequence.  Heads are independent.
+ *   - Batch size is one sequence (the serving calls at the end of this file take
+ *     several).  Heads are independent.
  *   - Numerics: bf16 Q/K/V/O, tensor-core products with fp32 accumulation, fp32
  *     softmax and scores; P is rounded to bf16 before the P.V product.
  */
@@ -261,6 +262,26 @@ dsa_status dsa_build_indices_static(const dsa_problem* p, const void* Q, const v
  * timeout the output of that launch is incomplete.  A diagnostic: a short bound
  * makes the abort path reachable without any fault. */
 dsa_status dsa_set_wait_limit(uint64_t limit_ns);
+
+/* ---------------------------------------------------------------------------
+ * Serving: what surrounds the sparse prefill of one long sequence.  Short prompts
+ * packed into one call, a paged cache of their keys and values in 8 bits, and the
+ * attention of each request's newest tokens over that cache.
+ * ------------------------------------------------------------------------- */
+
+/* Dense causal attention over packed sequences.  Q [Hq], K and V [Hkv] hold N packed
+ * rows (p->block is not used); rows cu_seqlens[s] .. cu_seqlens[s + 1] - 1 are sequence
+ * s, n_seq of them (device int32 [n_seq + 1], ascending, 0 <= cu <= N; lengths of 0 are
+ * fine).  Row i of a sequence attends to that sequence's rows j <= i:
+ *   O_i = sum_j softmax_j(q_i . k_j / sqrt(d)) v_j.
+ * Values that a row must not see never reach it, infinities and NaN among them.
+ * O: device bf16 with the problem's o strides; lse: optional device float [Hq * N].
+ * Rows of no sequence (behind the last, say) are left as they were.  A sequence whose
+ * bounds are malformed is skipped and reported as DSA_ERR_DEVICE.  A head stride of 0
+ * is DSA_ERR_INVALID_ARG unless there is one head. */
+dsa_status dsa_packed_prefill(const dsa_problem* p, const void* Q, const void* K, const void* V,
+                              const int32_t* cu_seqlens, int32_t n_seq, void* O, float* lse,
+                              dsa_stream stream);
 
 /* Static description of a status code. */
 const char* dsa_status_string(dsa_status s);
