@@ -17,9 +17,9 @@
 //   * TMEM (all 512 columns): S_A, S_B, O_A, O_B of 128 columns each; P overwrites the first
 //     64 columns of its S as bf16 pairs; S(t+1) is issued right after P(t) V(t), one thread's
 //     MMAs run in issue order;
-//   * the running maximum is raised only when it grows by more than 2^32 (log2 units below),
+//   * the running maximum is raised only when it grows by more than 2^8,
 //     so O is rescaled almost never: scaling all P of a row by one power of two changes no
-//     rounding, and l, O <= 2^53 |V| stay far inside fp32.
+//     rounding, and l <= 2^29 and O <= 2^29 |V| stay inside fp32.
 // V FIX: a hidden key has P = 0, but 0 x infinity is NaN.  The last key tile of an item holds
 // rows behind the sequence's end (another request's values) and keys that some rows must not
 // see; warp 10 zeroes the former, and zero the non-finite elements of the others, noting
@@ -39,7 +39,7 @@ constexpr int PACK_THREADS = 352;  // 11 warps: up to 184 registers a thread, wh
 constexpr uint32_t PACK_TMEM = 512;
 constexpr uint32_t PACK_O = 256;    // O of tile x at PACK_O + 128 x, S of tile x at 128 x
 constexpr int NITEM = 4;            // ItemInfo ring
-constexpr float PACK_RESCALE = 32.0f;
+constexpr float PACK_RESCALE = 8.0f;
 
 struct PackArgs {
   int Hq, G, T, nseq, npairs;
@@ -453,8 +453,13 @@ packed_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
         const float inv = (l > 0.f) ? 1.f / l : (l == 0.f ? 0.f : l);  // l is 0 without a key of weight, NaN stays
         const int64_t grow = (int64_t)start + (in ? row : 0);
         __nv_bfloat16* orow = a.O + (int64_t)h * a.o_hs + grow * a.o_ts;
-        const uint32_t* bad = im->bad[n - im->n[0]];
-        const uint32_t b0 = bad[0], b1 = bad[1], b2 = bad[2], b3 = bad[3];
+        // cleaned key tiles that this tile's rows see: the diagonal one, and tile A's diagonal one in front of it
+        const int first_bad = im->n[0] - 1;
+        uint32_t any_bad = 0;
+        for (int i = first_bad; i < n; ++i) {
+          const uint32_t* bad = im->bad[i - first_bad];
+          any_bad |= bad[0] | bad[1] | bad[2] | bad[3];
+        }
 #pragma unroll 1
         for (int c = 0; c < D / 32; ++c) {
           float o[32];
@@ -462,13 +467,13 @@ packed_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
           tmem_wait_ld();
 #pragma unroll
           for (int i = 0; i < 32; ++i) o[i] *= inv;
-          if ((b0 | b1 | b2 | b3) != 0u && in) {
-            // non-finite values of the diagonal tile's keys that this row sees
-            const __nv_bfloat16* v = a.V + (int64_t)(h / a.G) * a.v_hs + ((int64_t)start + (n - 1) * TN) * a.v_ts + c * 32;
+          if (any_bad != 0u && in) {
+            // non-finite values of those tiles' keys that this row sees
+            const __nv_bfloat16* v = a.V + (int64_t)(h / a.G) * a.v_hs + ((int64_t)start + first_bad * TN) * a.v_ts + c * 32;
+            const int seen = (n - 1 - first_bad) * TN + r;
 #pragma unroll 1
-            for (int j = 0; j <= r; ++j) {
-              const uint32_t word = j < 32 ? b0 : j < 64 ? b1 : j < 96 ? b2 : b3;
-              if (!((word >> (j & 31)) & 1u)) continue;
+            for (int j = 0; j <= seen; ++j) {
+              if (!((im->bad[j >> 7][(j >> 5) & 3] >> (j & 31)) & 1u)) continue;
 #pragma unroll
               for (int i = 0; i < 32; ++i) {
                 const float e = __bfloat162float(v[(int64_t)j * a.v_ts + i]);
