@@ -13,4 +13,5 @@ loudly if it has not been built (``python -m dynamic_sparse_attention_build_b200
 """
 from .api import (HostPrefill, IndexBuffers, alloc_indices, build_indices, count_pairs,  # noqa: F401
                   device_status, indices_from_lists, make_patterns, make_problem, sparse_prefill)
-from .serving import packed_prefill  # noqa: F401
+from .serving import (PageCache, Tables, build_tables, cache_attention, cache_write,  # noqa: F401
+                      packed_prefill)

@@ -35,7 +35,8 @@ KIND_CODES = {"ashape": DSA_KIND_ASHAPE, "vs": DSA_KIND_VS, "block_topk": DSA_KI
 EXPORTS = ("dsa_workspace_size", "dsa_build_indices", "dsa_sparse_prefill", "dsa_count_pairs",
            "dsa_get_device_status", "dsa_selftest_wait_timeout", "dsa_status_string",
            "dsa_last_cuda_error", "dsa_build_indices_static", "dsa_set_wait_limit",
-           "dsa_packed_prefill")
+           "dsa_packed_prefill", "dsa_build_tables", "dsa_cache_write", "dsa_cache_attention_workspace",
+           "dsa_cache_attention")
 
 
 class dsa_problem(ctypes.Structure):
@@ -75,6 +76,13 @@ class dsa_sizes(ctypes.Structure):
                 ("col_cap", ctypes.c_int64), ("workspace_bytes", ctypes.c_int64)]
 
 
+class dsa_cache(ctypes.Structure):
+    _fields_ = [("num_pages", ctypes.c_int32), ("Hkv", ctypes.c_int32), ("page", ctypes.c_int32), ("d", ctypes.c_int32),
+                ("page_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64), ("token_stride", ctypes.c_int64),
+                ("K", ctypes.c_void_p), ("V", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p)]
+
+
 _lib = None
 
 
@@ -101,12 +109,19 @@ def lib():
         L.dsa_packed_prefill.argtypes = [P(dsa_problem), ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p,
                                          ctypes.c_void_p, ctypes.c_int32, ctypes.c_void_p, ctypes.c_void_p,
                                          ctypes.c_void_p]
+        ptr, i32, i64 = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64
+        L.dsa_build_tables.argtypes = [i32, ptr, ptr, ptr, i32, ptr, ptr, i32, i32, i32, ptr, ptr, ptr, ptr, ptr]
+        L.dsa_cache_write.argtypes = [P(dsa_cache), ptr, ptr, i64, i64, i64, i64, ptr, i32, ptr]
+        L.dsa_cache_attention_workspace.argtypes = [i32]
+        L.dsa_cache_attention.argtypes = [P(dsa_cache), ptr, i32, i64, i64, ptr, i32, ptr, i32, i32, ptr, i64, i64, ptr,
+                                          ptr, ctypes.c_size_t, ptr]
         L.dsa_status_string.argtypes = [ctypes.c_int]
         L.dsa_status_string.restype = ctypes.c_char_p
         L.dsa_last_cuda_error.argtypes = []
         for name in EXPORTS:
             if name not in ("dsa_status_string",):
                 getattr(L, name).restype = ctypes.c_int if name != "dsa_last_cuda_error" else ctypes.c_int32
+        L.dsa_cache_attention_workspace.restype = i64
         _lib = L
     return _lib
 

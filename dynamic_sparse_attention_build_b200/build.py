@@ -10,7 +10,7 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 SOURCES = ["dsa_api.cu", "dsa_attn.cu", "dsa_index.cu", "dsa_noalloc.cu",
-           "dsa_pack.cu"]
+           "dsa_pack.cu", "dsa_cache.cu"]
 LIB = os.path.join(HERE, "libdsa.so")
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 

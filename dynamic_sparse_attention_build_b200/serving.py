@@ -1,5 +1,6 @@
 """Serving calls around the sparse prefill (marshalling only, like ``api``): dense attention
-over packed prompts.
+over packed prompts, the page tables of a paged cache, the store of keys and values in 8 bits,
+and the attention of new tokens over that cache.
 
 Token tensors are bf16 CUDA tensors shaped [heads, tokens, d] as in ``api``.  Arguments are
 checked here before the library sees a pointer: a wrong shape, type, device or layout raises
@@ -9,6 +10,8 @@ stream of the tensors' device); what it allocates belongs to that stream.
 from __future__ import annotations
 
 import contextlib
+import ctypes
+from dataclasses import dataclass, field
 
 import torch
 
@@ -20,15 +23,30 @@ def _need(ok, what):
         raise ValueError(what)
 
 
-@contextlib.contextmanager
-def _on(device, stream):
-    """The tensors' device and the call's stream made current: launches and allocations follow them."""
-    with torch.cuda.device(device):
-        if stream is None:
-            yield torch.cuda.current_stream(device).cuda_stream
-        else:
-            with torch.cuda.stream(stream):
-                yield stream.cuda_stream
+class _on:
+    """The tensors' device and the call's stream made current: launches and allocations follow
+    them.  Entering gives the stream's handle."""
+    __slots__ = ("device", "stream", "held")
+
+    def __init__(self, device, stream):
+        self.device, self.stream, self.held = device, stream, None
+
+    def __enter__(self):
+        if self.stream is None and torch.cuda.current_device() == self.device.index:
+            return torch.cuda.current_stream().cuda_stream
+        self.held = contextlib.ExitStack()
+        self.held.enter_context(torch.cuda.device(self.device))
+        if self.stream is None:
+            return torch.cuda.current_stream().cuda_stream
+        if self.stream.device != self.device:
+            self.held.close()
+            raise ValueError(f"the stream belongs to {self.stream.device}, the tensors to {self.device}")
+        self.held.enter_context(torch.cuda.stream(self.stream))
+        return self.stream.cuda_stream
+
+    def __exit__(self, *why):
+        if self.held is not None:
+            self.held.close()
 
 
 def _tokens(name, t, heads=None, tokens=None, d=None, device=None):
@@ -93,4 +111,156 @@ def packed_prefill(Q, K, V, cu_seqlens, O=None, lse=None, want_lse=False, stream
             B.check(B.dsa_packed_prefill(p, Q.data_ptr(), K.data_ptr(), V.data_ptr(), cu_seqlens.data_ptr(),
                                          cu_seqlens.numel() - 1, O.data_ptr(), lse.data_ptr() if lse is not None else None,
                                          st), "dsa_packed_prefill")
+    return O, lse
+
+
+PAGE_SIZES = (16, 32, 64, 128, 256)
+E4M3 = torch.float8_e4m3fn
+
+
+@dataclass(frozen=True, eq=False)
+class PageCache:
+    """Keys and values in 8 bits (``dsa_cache`` in include/dsa.h): K and V are float8_e4m3fn
+    [pages, Hkv, page, d] with equal strides and a contiguous last dimension (a
+    [pages, page, Hkv, d] tensor viewed with ``.transpose(1, 2)`` works too), k_scale and
+    v_scale float32 [pages, Hkv]."""
+    K: torch.Tensor
+    V: torch.Tensor
+    k_scale: torch.Tensor
+    v_scale: torch.Tensor
+    c: B.dsa_cache = field(init=False, repr=False)
+
+    def __post_init__(self):
+        K, V = self.K, self.V
+        for name, t in (("K", K), ("V", V)):
+            _need(isinstance(t, torch.Tensor) and t.dim() == 4, f"{name} must be a tensor [pages, Hkv, page, d]")
+            _need(t.is_cuda and t.device == K.device, f"{name} must be a CUDA tensor on one device with K")
+            _need(t.dtype == E4M3, f"{name} must be {E4M3}, not {t.dtype}")
+            _need(t.stride(3) == 1, f"{name}: the last dimension must be contiguous")
+        _need(K.shape == V.shape and K.stride() == V.stride(), "K and V must have one shape and one layout")
+        pages, Hkv, page, d = K.shape
+        _need(pages > 0 and Hkv > 0, "the cache is empty")
+        _need(page in PAGE_SIZES, f"a page has 16, 32, 64, 128 or 256 tokens, not {page}")
+        _need(d in (64, 128), f"d must be 64 or 128, not {d}")
+        for name, t in (("k_scale", self.k_scale), ("v_scale", self.v_scale)):
+            _need(isinstance(t, torch.Tensor) and t.dtype == torch.float32 and t.device == K.device
+                  and tuple(t.shape) == (pages, Hkv) and t.is_contiguous(),
+                  f"{name} must be a contiguous float32 tensor [{pages}, {Hkv}] on {K.device}")
+        token = K.stride(2)
+        head = K.stride(1) if Hkv > 1 else page * token
+        whole = K.stride(0) if pages > 1 else Hkv * page * token
+        _need(token >= d and head >= d and whole >= d, "pages, heads and tokens of the cache must not overlap")
+        object.__setattr__(self, "c", B.dsa_cache(pages, Hkv, page, d, whole, head, token, K.data_ptr(), V.data_ptr(),
+                                                  self.k_scale.data_ptr(), self.v_scale.data_ptr()))
+
+    @classmethod
+    def empty(cls, pages, Hkv, page, d, device="cuda"):
+        """A cache of zeros, every scale at its smallest."""
+        new = lambda: torch.zeros(pages, Hkv, page, d, dtype=torch.uint8, device=device).view(E4M3)  # noqa: E731
+        scale = lambda: torch.full((pages, Hkv), 2.0 ** -60, dtype=torch.float32, device=device)  # noqa: E731
+        return cls(new(), new(), scale(), scale())
+
+
+@dataclass
+class Tables:
+    """What ``build_tables`` gives: the slot of each new token (-1 behind the last), where each
+    request's new tokens begin, the requests' new lengths and the free pages that are left."""
+    slots: torch.Tensor
+    cu_seqlens: torch.Tensor
+    lens: torch.Tensor
+    free_count: torch.Tensor
+
+
+def build_tables(lens, new_lens, free_pages, free_count, block_table, page, max_tokens, out=None, stream=None):
+    """Pages and slots for the tokens that each request gets next; returns ``Tables``.
+
+    lens, new_lens: int32 [B], the tokens that each request has and gets (a negative number
+    ends it and frees its pages); block_table int32 [B, W] and the stack of free pages
+    (free_pages int32 [F], free_count int32 [1]) are updated in place.  ``out`` takes the
+    results (its ``lens`` and ``free_count`` may be the call's own).  If the pages, the table's
+    width or ``max_tokens`` do not suffice, nothing changes, no token has a slot, and
+    ``device_status`` says DSA_ERR_CAPACITY."""
+    _need(isinstance(lens, torch.Tensor) and lens.dim() == 1 and lens.numel() > 0, "lens must be an int32 tensor [requests]")
+    _need(lens.is_cuda, "lens must be a CUDA tensor")
+    dev, n = lens.device, lens.numel()
+    _ints("lens", lens, (n,), dev)
+    _ints("new_lens", new_lens, (n,), dev)
+    _need(isinstance(free_pages, torch.Tensor) and free_pages.dim() == 1 and free_pages.numel() > 0,
+          "free_pages must be an int32 tensor [pages]")
+    _ints("free_pages", free_pages, free_pages.shape, dev)
+    _ints("free_count", free_count, (1,), dev)
+    _need(isinstance(block_table, torch.Tensor) and block_table.dim() == 2 and block_table.shape[1] > 0,
+          "block_table must be an int32 tensor [requests, pages of a request]")
+    _ints("block_table", block_table, (n, block_table.shape[1]), dev)
+    _need(page in PAGE_SIZES, f"a page has 16, 32, 64, 128 or 256 tokens, not {page}")
+    _need(max_tokens >= 0, "max_tokens must not be negative")
+    if out is not None:
+        _ints("out.slots", out.slots, (max_tokens,), dev)
+        _ints("out.cu_seqlens", out.cu_seqlens, (n + 1,), dev)
+        _ints("out.lens", out.lens, (n,), dev)
+        _ints("out.free_count", out.free_count, (1,), dev)
+    with _on(dev, stream) as st:
+        if out is None:
+            new = lambda k: torch.empty(k, dtype=torch.int32, device=dev)  # noqa: E731
+            out = Tables(new(max_tokens), new(n + 1), new(n), new(1))
+        B.check(B.lib().dsa_build_tables(
+            n, lens.data_ptr(), new_lens.data_ptr(), free_pages.data_ptr(), free_pages.numel(), free_count.data_ptr(),
+            block_table.data_ptr(), block_table.shape[1], page, max_tokens, out.slots.data_ptr(),
+            out.cu_seqlens.data_ptr(), out.lens.data_ptr(), out.free_count.data_ptr(), st), "dsa_build_tables")
+    return out
+
+
+def cache_write(K, V, slots, cache, stream=None):
+    """Stores the rows of K and V [Hkv, T, d] at ``slots`` (int32 [T], from ``build_tables``;
+    negative ones are passed over) in the cache, in e4m3 with one power-of-two scale per page
+    and head."""
+    c = cache.c
+    dev = cache.K.device
+    _tokens("K", K, c.Hkv, None, c.d, dev)
+    T = K.shape[1]
+    _tokens("V", V, c.Hkv, T, c.d, dev)
+    _ints("slots", slots, (T,), dev)
+    if T == 0:
+        return
+    with _on(dev, stream) as st:
+        B.check(B.lib().dsa_cache_write(ctypes.byref(c), K.data_ptr(), V.data_ptr(), *_strides(K), *_strides(V),
+                                        slots.data_ptr(), T, st), "dsa_cache_write")
+
+
+def cache_attention(Q, cache, block_table, lens, n_q=1, O=None, lse=None, want_lse=False, workspace=None, stream=None):
+    """Attention of each request's newest ``n_q`` tokens over its cached keys; returns (O, lse or None).
+
+    Q [Hq, B * n_q, d] holds the tokens request by request; lens (int32 [B]) counts the tokens
+    that each request has in the cache, the new ones among them (``cache_write`` first), and
+    block_table (int32 [B, W]) names their pages.  Token i of a request sees its keys up to
+    lens - n_q + i; a token that sees none has O = 0 and lse = -inf.  ``workspace`` (bytes,
+    as many as ``dsa_cache_attention_workspace`` says) is allocated here if it is not given."""
+    c = cache.c
+    dev = cache.K.device
+    _tokens("Q", Q, None, None, c.d, dev)
+    Hq, T, d = Q.shape
+    _need(Hq > 0 and Hq % c.Hkv == 0, f"{Hq} query heads do not divide into {c.Hkv} KV heads")
+    _need(isinstance(block_table, torch.Tensor) and block_table.dim() == 2 and block_table.shape[1] > 0,
+          "block_table must be an int32 tensor [requests, pages of a request]")
+    n, width = block_table.shape
+    _ints("block_table", block_table, (n, width), dev)
+    _ints("lens", lens, (n,), dev)
+    _need(n_q >= 1 and T == n * n_q, f"Q has {T} rows, not {n_q} for each of {n} requests")
+    if O is not None:
+        _tokens("O", O, Hq, T, d, dev)
+    need = B.lib().dsa_cache_attention_workspace(d)
+    if workspace is not None:
+        _need(workspace.device == dev and workspace.is_contiguous()
+              and workspace.numel() * workspace.element_size() >= need, f"workspace must hold {need} bytes on {dev}")
+    with _on(dev, stream) as st:
+        if O is None:
+            O = torch.empty_like(Q, memory_format=torch.contiguous_format)
+        lse = _lse(lse, want_lse, (Hq, T), dev)
+        if workspace is None:
+            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+        if n > 0:
+            B.check(B.lib().dsa_cache_attention(
+                ctypes.byref(c), Q.data_ptr(), Hq, *_strides(Q), block_table.data_ptr(), width, lens.data_ptr(), n, n_q,
+                O.data_ptr(), *_strides(O), lse.data_ptr() if lse is not None else None, workspace.data_ptr(),
+                workspace.numel() * workspace.element_size(), st), "dsa_cache_attention")
     return O, lse

@@ -283,6 +283,84 @@ dsa_status dsa_packed_prefill(const dsa_problem* p, const void* Q, const void* K
                               const int32_t* cu_seqlens, int32_t n_seq, void* O, float* lse,
                               dsa_stream stream);
 
+/*
+ * A paged cache of keys and values in 8 bits.  K and V hold num_pages pages of `page`
+ * tokens (16, 32, 64, 128 or 256) for each of Hkv heads, e4m3 values of head dimension
+ * d in {64, 128}: value x of token t of a page and head is at
+ *   page * page_stride + head * head_stride + t * token_stride + x   (bytes, multiples
+ * of 16; base pointers 16-byte aligned), and stands for itself times the page's scale
+ * k_scale / v_scale [num_pages * Hkv], a float in 2^-64 .. 2^64.  dsa_cache_write
+ * writes powers of two in 2^-60 .. 2^60.  A page's scales need a valid value (2^-60,
+ * say) before tokens are first written behind its beginning.
+ */
+typedef struct dsa_cache {
+    int32_t num_pages, Hkv, page, d;
+    int64_t page_stride, head_stride, token_stride;
+    void* K;
+    void* V;
+    float* k_scale;
+    float* v_scale;
+} dsa_cache;
+
+/* Page tables of n_req requests (at most 4096), built on the GPU from their lengths.
+ * Request b holds lens[b] tokens in the pages block_table[b * width + 0, 1, ..] and now
+ * gets new_lens[b] more, or ends (new_lens[b] < 0).  free_pages [free_cap] is a stack of
+ * free pages, its top at free_count[0] - 1.  In this order:
+ *   - the pages of the requests that end go on the stack, request by request;
+ *   - each other request takes the pages it needs from the top, request by request, and
+ *     its table row grows by them;
+ *   - cu_seqlens [n_req + 1]: sums of the new tokens (an ended request has none);
+ *   - slots [max_tokens]: token i of request b (row cu_seqlens[b] + i) goes to slot
+ *     block_table[b][(lens[b] + i) / page] * page + (lens[b] + i) % page; rows behind
+ *     the last token get -1;
+ *   - lens_out [n_req]: the new lengths (0 for an ended request); free_count_out [1].
+ * lens_out may be lens, and free_count_out may be free_count.  All arrays are device
+ * int32.  If the stack runs out or over, a row of the table would not fit, or there are
+ * more than max_tokens new tokens, nothing is taken or given back: DSA_ERR_CAPACITY is
+ * reported (DSA_ERR_DEVICE for a negative length), every slot is -1, cu_seqlens is 0 and
+ * lengths and count are as before.  A slot whose page number is no page is -1 and
+ * reported. */
+dsa_status dsa_build_tables(int32_t n_req, const int32_t* lens, const int32_t* new_lens, int32_t* free_pages,
+                            int32_t free_cap, const int32_t* free_count, int32_t* block_table, int32_t width,
+                            int32_t page, int32_t max_tokens, int32_t* slots, int32_t* cu_seqlens,
+                            int32_t* lens_out, int32_t* free_count_out, dsa_stream stream);
+
+/* Stores n_tokens rows of K and V (device bf16, [Hkv] heads; strides in elements,
+ * multiples of 8) in the cache; row t goes to slots[t] = page * page_size + place,
+ * negative slots are passed over.  For each page and head the scale becomes the smallest
+ * power of two s with max |x| <= 448 s over the page's new rows, or the scale the page has
+ * if that is larger and rows before the new ones are kept; kept rows are rounded again
+ * where the scale grows.  Values are rounded to nearest even; infinities become the
+ * largest value, NaN stays.
+ * The rows of one page follow each other, in the call as in the page (slots as
+ * dsa_build_tables makes them); rows of a page behind the last new one count as empty.  A
+ * page named in two places of one call ends with undefined contents.  A slot beyond the
+ * cache, or a scale outside its range that has to be kept, is reported as DSA_ERR_DEVICE. */
+dsa_status dsa_cache_write(const dsa_cache* cache, const void* K, const void* V, int64_t k_head_stride,
+                           int64_t k_token_stride, int64_t v_head_stride, int64_t v_token_stride,
+                           const int32_t* slots, int32_t n_tokens, dsa_stream stream);
+
+/* Bytes of workspace that dsa_cache_attention needs for head dimension d.  Pure host. */
+int64_t dsa_cache_attention_workspace(int32_t d);
+
+/* Attention of the newest n_q tokens of each request over the cache.  Request b has
+ * lens[b] tokens in the cache (its newest ones among them) in the pages of its row of
+ * block_table [n_req][width]; Q and O hold n_req * n_q rows of Hq heads (a multiple of the
+ * cache's Hkv), token i of request b at row b * n_q + i, which sees the keys
+ * j <= lens[b] - n_q + i:
+ *   O = sum_j softmax_j(q . k_j / sqrt(d)) v_j,   lse [Hq * n_req * n_q] (optional).
+ * A row without keys gives O = 0 and lse = -inf.  Values that a row must not see (other
+ * requests' pages, the rest of the last page) never reach it.  A length that the table row
+ * cannot hold is cut, and a page number or scale that is none is skipped; both are reported
+ * as DSA_ERR_DEVICE.  workspace: device scratch (16-byte aligned) of at least the bytes
+ * above; its contents on entry do not matter, and calls whose work overlaps on the GPU
+ * need one each. */
+dsa_status dsa_cache_attention(const dsa_cache* cache, const void* Q, int32_t Hq, int64_t q_head_stride,
+                               int64_t q_token_stride, const int32_t* block_table, int32_t width,
+                               const int32_t* lens, int32_t n_req, int32_t n_q, void* O, int64_t o_head_stride,
+                               int64_t o_token_stride, float* lse, void* workspace, size_t workspace_bytes,
+                               dsa_stream stream);
+
 /* Static description of a status code. */
 const char* dsa_status_string(dsa_status s);
 

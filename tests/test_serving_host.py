@@ -1,0 +1,157 @@
+"""Host-side checks of the serving calls (no GPU): the library refuses bad arguments before any
+launch, the Python layer refuses tensors that are not on a GPU, and the plain forms that the GPU
+tests rely on follow hand-worked examples."""
+import ctypes
+import os
+
+import pytest
+import torch
+
+from tests import _serving as plain
+
+
+@pytest.fixture(scope="module")
+def B():
+    from dynamic_sparse_attention_build_b200 import _binding
+    if not os.path.exists(_binding.LIB_PATH):
+        from dynamic_sparse_attention_build_b200 import build
+        build.build()
+    _binding.lib()
+    return _binding
+
+
+A = 1 << 20  # an aligned address that is never followed: every call below is refused on the host
+
+
+def problem(B, **kw):
+    v = dict(Hq=4, Hkv=2, N=100, d=128, block=64, reserved=0, q_head_stride=12800, q_token_stride=128,
+             k_head_stride=12800, k_token_stride=128, v_head_stride=12800, v_token_stride=128, o_head_stride=12800,
+             o_token_stride=128)
+    v.update(kw)
+    return B.dsa_problem(**v)
+
+
+@pytest.mark.parametrize("change, args", [
+    (dict(Hq=5), {}), (dict(N=0), {}), (dict(q_token_stride=120), {}), (dict(v_token_stride=132), {}),
+    (dict(q_head_stride=0), {}), (dict(k_head_stride=0), {}), (dict(v_head_stride=0), {}), (dict(o_head_stride=0), {}),
+    ({}, dict(Q=None)), ({}, dict(V=A + 8)), ({}, dict(O=A + 2)), ({}, dict(cu=None)), ({}, dict(n=-1)),
+])
+def test_packed_prefill_refuses(B, change, args):
+    a = dict(Q=A, K=A, V=A, cu=A, n=3, O=A)
+    a.update(args)
+    got = B.lib().dsa_packed_prefill(ctypes.byref(problem(B, **change)), a["Q"], a["K"], a["V"], a["cu"], a["n"], a["O"],
+                                     None, None)
+    assert got == B.DSA_ERR_INVALID_ARG
+
+
+def test_packed_prefill_refuses_unsupported_sizes(B):
+    for change in (dict(d=96), dict(N=(1 << 21) + 1), dict(Hq=8192, Hkv=8192)):
+        assert B.lib().dsa_packed_prefill(ctypes.byref(problem(B, **change)), A, A, A, A, 1, A, None, None) \
+            == B.DSA_ERR_UNSUPPORTED
+
+
+@pytest.mark.parametrize("change, want", [
+    (dict(n=0), 1), (dict(width=0), 1), (dict(cap=0), 1), (dict(tokens=-1), 1), (dict(page=48), 1), (dict(page=512), 1),
+    (dict(lens=None), 1), (dict(slots=None), 1), (dict(table=None), 1), (dict(n=4097), 2), (dict(tokens=(1 << 30) + 1), 2),
+])
+def test_build_tables_refuses(B, change, want):
+    a = dict(n=3, lens=A, new=A, free=A, cap=9, count=A, table=A, width=4, page=64, tokens=10, slots=A, cu=A, out=A, left=A)
+    a.update(change)
+    assert B.lib().dsa_build_tables(*a.values(), None) == want
+
+
+def cache(B, **kw):
+    v = dict(num_pages=9, Hkv=2, page=64, d=128, page_stride=2 * 64 * 128, head_stride=64 * 128, token_stride=128, K=A, V=A,
+             k_scale=A, v_scale=A)
+    v.update(kw)
+    return B.dsa_cache(**v)
+
+
+BAD_CACHES = [(dict(num_pages=0), 1), (dict(page=24), 1), (dict(d=32), 2), (dict(Hkv=0), 1), (dict(K=None), 1),
+              (dict(V=A + 8), 1), (dict(k_scale=None), 1), (dict(token_stride=64), 1), (dict(token_stride=136), 1),
+              (dict(head_stride=64), 1), (dict(page_stride=100), 1), (dict(page_stride=0), 1), (dict(Hkv=4097), 2),
+              (dict(num_pages=1 << 26), 2)]
+
+
+@pytest.mark.parametrize("change, want", BAD_CACHES)
+def test_bad_caches_are_refused(B, change, want):
+    c = cache(B, **change)
+    assert B.lib().dsa_cache_write(ctypes.byref(c), A, A, 512, 128, 512, 128, A, 4, None) == want
+    assert B.lib().dsa_cache_attention(ctypes.byref(c), A, 4, 512, 128, A, 3, A, 2, 1, A, 512, 128, None, A, 1 << 30, None) == want
+
+
+@pytest.mark.parametrize("change", [dict(T=-1), dict(K=None), dict(V=A + 8), dict(slots=None), dict(kt=100), dict(vh=4)])
+def test_cache_write_refuses(B, change):
+    a = dict(K=A, V=A, kh=512, kt=128, vh=512, vt=128, slots=A, T=4)
+    a.update(change)
+    assert B.lib().dsa_cache_write(ctypes.byref(cache(B)), *a.values(), None) == B.DSA_ERR_INVALID_ARG
+
+
+@pytest.mark.parametrize("change, want", [
+    (dict(Hq=3), 1), (dict(Hq=0), 1), (dict(n=-1), 1), (dict(nq=0), 1), (dict(width=0), 1), (dict(Q=None), 1),
+    (dict(O=A + 4), 1), (dict(qt=100), 1), (dict(ot=64), 1), (dict(oh=0), 1), (dict(ws=None), 1), (dict(size=100), 3),
+    (dict(n=4097), 2), (dict(width=1 << 26), 2), (dict(Hq=8192), 2),
+])
+def test_cache_attention_refuses(B, change, want):
+    a = dict(Q=A, Hq=4, qh=512, qt=128, table=A, width=3, lens=A, n=2, nq=1, O=A, oh=512, ot=128, lse=None, ws=A, size=1 << 30)
+    a.update(change)
+    assert B.lib().dsa_cache_attention(ctypes.byref(cache(B)), *a.values(), None) == want
+
+
+def test_nothing_to_do_is_no_error(B):
+    assert B.lib().dsa_cache_write(ctypes.byref(cache(B)), None, None, 0, 0, 0, 0, None, 0, None) == B.DSA_OK
+    assert B.lib().dsa_packed_prefill(ctypes.byref(problem(B)), A, A, A, None, 0, A, None, None) == B.DSA_OK
+    assert B.lib().dsa_cache_attention_workspace(128) > B.lib().dsa_cache_attention_workspace(64) > 0
+
+
+def test_host_tensors_are_refused(B):
+    import dynamic_sparse_attention_build_b200 as dsa
+    t = torch.zeros(2, 5, 64, dtype=torch.bfloat16)
+    i = torch.zeros(3, dtype=torch.int32)
+    with pytest.raises(ValueError, match="CUDA"):
+        dsa.packed_prefill(t, t, t, i)
+    with pytest.raises(ValueError, match="CUDA"):
+        dsa.build_tables(i, i, i, i[:1], i[:, None], 16, 4)
+    with pytest.raises(ValueError, match="CUDA"):
+        dsa.PageCache.empty(3, 2, 16, 64, device="cpu")
+
+
+# ---- the plain forms ------------------------------------------------------------------------
+def test_plain_tables_hand_example():
+    # page 4; request 0 has 3 tokens in page 7 and gets 6 more, request 1 (pages 2, 5) ends, request 2 is new
+    got = plain.tables_plain([3, 5, 0], [6, -1, 2], [9, 8, -1, -1, -1], 2, [[7, -1, -1], [2, 5, -1], [-1, -1, -1]], 4, 10)
+    # 2 and 5 go on the stack [9, 8, 2, 5]; request 0 takes 5 and 2, request 2 takes 8
+    assert got[0] == [31, 20, 21, 22, 23, 8, 32, 33, -1, -1]
+    assert got[1] == [0, 6, 6, 8] and got[2] == [9, 0, 2] and got[3] == 1
+    assert got[4] == [[7, 5, 2], [2, 5, -1], [8, -1, -1]] and got[6]
+    # one page too few: nothing changes
+    got = plain.tables_plain([0], [9], [1, 2], 2, [[-1, -1, -1]], 4, 10)
+    assert got == ([-1] * 10, [0, 0], [0], 2, [[-1, -1, -1]], [1, 2], False)
+
+
+def test_plain_e4m3_matches_torch_casts():
+    every = torch.arange(256, dtype=torch.uint8).view(torch.float8_e4m3fn).double()
+    every = every[torch.isfinite(every)]
+    assert torch.equal(plain.e4m3_64(every), every)
+    mids = (torch.sort(every).values[1:] + torch.sort(every).values[:-1]) / 2
+    x = torch.cat([mids, mids * (1 + 2 ** -20), mids * (1 - 2 ** -20), torch.linspace(-448, 448, 999, dtype=torch.float64)])
+    x = x.float()
+    assert torch.equal(plain.e4m3_64(x.double()), x.to(torch.float8_e4m3fn).double())
+    assert plain.power_for(0.0) == 2.0 ** -60 and plain.power_for(448.0) == 1.0 and plain.power_for(449.0) == 2.0
+    assert plain.power_for(1e38) == 2.0 ** 60
+
+
+def test_plain_attention_follows_differences():
+    """d lse / d s_j is the weight of key j: the plain form's weights against differences."""
+    g = torch.Generator().manual_seed(3)
+    q, k, v = (torch.randn(n, 8, generator=g, dtype=torch.float64) for n in (1, 5, 5))
+    last = torch.tensor([3])
+    o, lse, _, _, w = plain.attention64(q, k, v, last)
+    h = 1e-6
+    for j in range(5):
+        k2 = k.clone()
+        k2[j] += h * q[0]  # the score grows by h |q|^2 / sqrt(d)
+        ds = h * float(q[0] @ q[0]) / 8 ** 0.5
+        assert abs((float(plain.attention64(q, k2, v, last)[1]) - float(lse)) / ds - float(w[0, j])) < 1e-5
+    assert float(w[0, 4]) == 0 and abs(float(w.sum()) - 1) < 1e-12
+    assert torch.allclose(o, w @ v)
