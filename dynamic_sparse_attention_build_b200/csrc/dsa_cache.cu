@@ -941,20 +941,12 @@ dsa_status validate_cache(const dsa_cache* c) {
   return DSA_OK;
 }
 
-dsa_status sm_count(int* sms) {
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e == cudaSuccess) e = cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev);
-  return e == cudaSuccess ? DSA_OK : cuda_fail(e);
-}
-
 template <int D, bool R8>
 dsa_status launch_attend(AttendArgs& a, cudaStream_t stream) {
-  int sms = 0;
-  dsa_status s = sm_count(&sms);
-  if (s != DSA_OK) return s;
+  int dev = 0, sms = 0;
+  cudaError_t e = serve_sms(&dev, &sms);
+  if (e == cudaSuccess) e = serve_allow_smem<k_cache_attend<D, R8>>(dev, AttendSmem<D>::bytes(MAX_REQ));
   const int smem = AttendSmem<D>::bytes(a.n_req);
-  cudaError_t e = cudaFuncSetAttribute(k_cache_attend<D, R8>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   const int grid = min(AT_PER_SM * sms, AT_MAX_CTAS);
   if (e == cudaSuccess) e = launch_pdl(k_cache_attend<D, R8>, dim3(grid), dim3(AT_THREADS), (size_t)smem, stream, a);
   const int rows = min(16, a.n_q * a.G);
@@ -1002,7 +994,9 @@ dsa_status dsa_build_tables(int32_t n_req, const int32_t* lens, const int32_t* n
   int ctas = 1;
   while (ctas < 8 && ctas * TAB_THREADS * 8 < max_tokens) ctas *= 2;
   const size_t smem = (size_t)(4 * n_req + 3) * 4;
-  cudaError_t e = cudaFuncSetAttribute(k_build_tables, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  int dev = 0, sms = 0;
+  cudaError_t e = serve_sms(&dev, &sms);
+  if (e == cudaSuccess) e = serve_allow_smem<k_build_tables>(dev, (4 * MAX_REQ + 3) * 4);
   if (e == cudaSuccess) e = serve_launch_cluster(k_build_tables, dim3(ctas), dim3(TAB_THREADS), ctas, smem, (cudaStream_t)stream, a);
   if (e == cudaSuccess) e = cudaGetLastError();
   return e == cudaSuccess ? DSA_OK : cuda_fail(e);

@@ -541,10 +541,9 @@ dsa_status launch_packed(const dsa_problem& p, const void* Q, const void* K, con
   a.scale_log2 = (float)(1.4426950408889634 / sqrt((double)D));
   a.status = status;
   a.wait_limit_ns = wait_limit_ns();
-  cudaError_t e = cudaFuncSetAttribute(packed_attn_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, PackSmem<D>::BYTES);
   int dev = 0, sms = 0;
-  if (e == cudaSuccess) e = cudaGetDevice(&dev);
-  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  cudaError_t e = serve_sms(&dev, &sms);
+  if (e == cudaSuccess) e = serve_allow_smem<packed_attn_kernel<D>>(dev, PackSmem<D>::BYTES);
   if (e != cudaSuccess) return cuda_fail(e);
   // the lengths are on the device: as many items as the rows could need at most
   const int64_t rows = (a.G & 1) == 0 ? TM : 2 * TM;

@@ -1,6 +1,8 @@
 // Device helpers shared by the serving kernels (packed prefill, page tables, 8-bit cache).
 #pragma once
 
+#include <atomic>
+
 #include "dsa_common.cuh"
 #include "dsa_internal.h"
 
@@ -31,6 +33,31 @@ inline cudaError_t serve_launch_cluster(void (*kernel)(KArgs...), dim3 grid, dim
   cfg.attrs = attr;
   cfg.numAttrs = 2;
   return cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...);
+}
+
+// SMs of the current device, looked up once per device (an attribute costs a driver call).
+inline cudaError_t serve_sms(int* dev, int* sms) {
+  static std::atomic<int> known[64];
+  cudaError_t e = cudaGetDevice(dev);
+  if (e != cudaSuccess) return e;
+  std::atomic<int>* k = *dev < 64 ? &known[*dev] : nullptr;
+  *sms = k ? k->load(std::memory_order_relaxed) : 0;
+  if (*sms == 0) {
+    e = cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, *dev);
+    if (e == cudaSuccess && k) k->store(*sms, std::memory_order_relaxed);
+  }
+  return e;
+}
+
+// Lets a kernel use `bytes` of dynamic shared memory on device `dev`, once per device.
+template <auto Kernel>
+inline cudaError_t serve_allow_smem(int dev, int bytes) {
+  static std::atomic<uint64_t> done;
+  const uint64_t bit = dev < 64 ? uint64_t(1) << dev : 0;
+  if (done.load(std::memory_order_relaxed) & bit) return cudaSuccess;
+  const cudaError_t e = cudaFuncSetAttribute(Kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
+  return e;
 }
 
 inline bool serve_aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
