@@ -9,20 +9,28 @@
 // Design (persistent, one CTA per SM; an item = two 128-row query tiles that walk the same keys):
 //   * the two tiles are the same rows of two query heads of one KV head when G is even, else
 //     two adjacent row tiles of one head: each K and V tile (128 keys) is loaded once for both;
-//   * warp 8 (whole) finds the items, one lane loads Q and streams K and V through a ring of
-//     NST stages with TMA; warp 9 (one thread) issues the tcgen05.mma; warps 0-3 run tile A's
-//     softmax and epilogue, warps 4-7 tile B's (one thread per row); while one tile is in its
-//     softmax the tensor core works on the other;
-//   * warp 10 cleans the V tiles that reach past what a row may see (see V FIX below);
-//   * TMEM (all 512 columns): S_A, S_B, O_A, O_B of 128 columns each; P overwrites the first
-//     64 columns of its S as bf16 pairs; S(t+1) is issued right after P(t) V(t), one thread's
-//     MMAs run in issue order;
-//   * the running maximum is raised only when it grows by more than 2^8,
-//     so O is rescaled almost never: scaling all P of a row by one power of two changes no
-//     rounding, and l <= 2^29 and O <= 2^29 |V| stay inside fp32.
-// V FIX: a hidden key has P = 0, but 0 x infinity is NaN.  The last key tile of an item holds
+//   * warps 0-3 run tile A's softmax and epilogue, warps 4-7 tile B's (one thread per row);
+//     warp 8 finds the items, one lane of it streams K and V through a ring of NST stages with
+//     TMA; warps 9 and 10 issue the tcgen05.mma of tile A and of tile B; warps 11-14 clean the V
+//     tiles that reach past what a row may see (V FIX below);
+//   * TMEM (all 512 columns): S of each tile in two halves of 64 keys, O_A, O_B of 128 columns;
+//     P overwrites the first 32 columns of its half as bf16 pairs.  A half's next S = Q K^T goes
+//     out right behind its P V, while the softmax works on the other half;
+//   * the running maximum is raised only when it grows by more than 2^8, so O is rescaled almost
+//     never: a row's weights may be up to 2^8 instead of 1, relative roundings are the same, and
+//     l <= 2^29 and O <= 2^29 |V| stay inside fp32.
+// What bounds it: MMA operands and TMA together move about 320 KB of shared memory per 128 keys of an
+// item (2500 cycles at 128 bytes), the weights' exponentials take 2048 (16 a cycle); a step of 128
+// keys takes 3650 at 32K tokens.  Steps that led here (32 query heads on 8, d 128, one sequence of 32768):
+//   one MMA thread, whole tiles of S: 9.0 ms.  The chain P -> P V -> S -> softmax was a step's time
+//     (4860 cycles), and the issuing thread was busy for 2700 of them;
+//   halves of 64 keys with one thread issuing: 12.8 ms (issue-bound); descriptors as uniform values of a
+//     whole warp, one lane elected: 10.0 ms; a warp for each tile: 8.1 ms.
+//   For d 64, where the softmax is the bound, 5 of 16 exponentials as polynomials: 0.269 -> 0.235 ms
+//     (16 heads, 8192 tokens); for d 128 that changes nothing.
+// V FIX: a hidden key has P = 0, but 0 x infinity is NaN.  The last key tile of a row tile holds
 // rows behind the sequence's end (another request's values) and keys that some rows must not
-// see; warp 10 zeroes the former, and zero the non-finite elements of the others, noting
+// see; warps 11-14 zero the former, and zero the non-finite elements of the others, noting
 // their rows; the epilogue adds those elements to the rows that do see them.
 // No cluster, no multicast; every wait is bounded (status word + early exit).
 #include "dsa_common.cuh"
@@ -34,11 +42,16 @@ namespace {
 
 constexpr int TM = 128;             // query rows of a tile
 constexpr int TN = 128;             // keys of a tile
+constexpr int TH = 64;              // keys of half a tile: what one softmax step takes
 constexpr int SLAB = 128 * 128;     // bytes of 128 rows x 64 bf16 columns
-constexpr int PACK_THREADS = 352;  // 11 warps: up to 184 registers a thread, which the softmax needs
+constexpr int CLEAN_WARPS = 4;
+constexpr int PACK_THREADS = 352 + 32 * CLEAN_WARPS;
 constexpr uint32_t PACK_TMEM = 512;
 constexpr uint32_t PACK_O = 256;    // O of tile x at PACK_O + 128 x, S of tile x at 128 x
 constexpr int NITEM = 4;            // ItemInfo ring
+// Barriers for cleaned V tiles, used in turn.  One MMA warp may be up to two cleaned tiles ahead of the other: it
+// cannot pass the next item's Q before the other has issued all of this item's Q K^T, and an item has two of them.
+constexpr int NFIX = 4;
 constexpr float PACK_RESCALE = 8.0f;
 
 struct PackArgs {
@@ -67,36 +80,60 @@ struct PackItem {
 template <int D>
 struct PackSmem {
   static constexpr int DS = D / 64;
-  static constexpr int NST = D == 128 ? 5 : 10;
+    static constexpr int NST = D == 128 ? 5 : 10;
   static constexpr int STAGE = DS * SLAB;
   static constexpr int Q_OFF = 0;
   static constexpr int KV_OFF = 2 * STAGE;
   static constexpr int ITEM_OFF = KV_OFF + NST * STAGE;
   static constexpr int BAR_OFF = ITEM_OFF + NITEM * (int)sizeof(PackItem);
-  static constexpr int NBAR = 2 * NST + 2 * NITEM + 11;
+  static constexpr int NBAR = 2 * NST + 2 * NITEM + 18 + NFIX;
   static constexpr int MISC_OFF = BAR_OFF + NBAR * 8;
   static constexpr int BYTES = MISC_OFF + 32 + 1024;
   static_assert(BYTES <= 232448, "shared memory");
   static_assert(sizeof(PackItem) % 8 == 0, "barrier alignment");
   // barriers
-  static constexpr int QFULL = 0, QEMPTY = 1, SFULL = 2, PFULL = 4, ODONE = 6, FIXREQ = 8, VFIX = 9, DRAIN = 10;
-  static constexpr int ITEMFULL = 11, ITEMFREE = ITEMFULL + NITEM;
+  // (SFULL, PFULL and ODONE: 2 * row tile + half.  A parity tells only neighbouring phases apart; with one barrier
+  // for each half, no one waits for a phase while the one behind it could be over.)
+  static constexpr int QFULL = 0, QEMPTY = 1, SFULL = 2, PFULL = 6, ODONE = 10, FIXREQ = 14, DRAIN = 16, VFIX = 18;
+  static constexpr int ITEMFULL = VFIX + NFIX, ITEMFREE = ITEMFULL + NITEM;
   static constexpr int FULL = ITEMFREE + NITEM, EMPTY = FULL + NST;
 };
 
-// S = Q K^T (both K-major, 128-byte swizzle): D / 16 k-steps.
-template <int D>
-__device__ __forceinline__ void pack_mma_qk(uint32_t d, uint64_t a0, uint64_t b0, uint32_t idesc) {
-#pragma unroll
-  for (int k = 0; k < D / 16; ++k) {
-    const uint64_t off = (uint64_t)((k >> 2) * (SLAB >> 4) + (k & 3) * 2);
-    tc_mma_f16(d, a0 + off, b0 + off, idesc, k > 0 ? 1u : 0u);
-  }
+// The whole MMA warp runs the code around these, so that descriptors and addresses are uniform values;
+// one elected lane issues.
+__device__ __forceinline__ bool pack_elect() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+  return p != 0;
 }
-// O (+)= P V: P from TMEM, V MN-major, 8 k-steps of 16 keys.
-__device__ __forceinline__ void pack_mma_pv(uint32_t d, uint32_t p, uint64_t b0, uint32_t idesc, uint32_t acc) {
+// S = Q K^T for 64 keys (both K-major, 128-byte swizzle): D / 16 k-steps.  a, b: low words of the descriptors.
+template <int D>
+__device__ __forceinline__ void pack_mma_qk(uint32_t d, uint32_t a, uint32_t b, uint32_t hi, uint32_t idesc) {
+  if (pack_elect()) {
 #pragma unroll
-  for (int k = 0; k < TN / 16; ++k) tc_mma_f16_ts(d, p + 8 * k, b0 + (uint64_t)(k * (2048 >> 4)), idesc, k > 0 ? 1u : acc);
+    for (int k = 0; k < D / 16; ++k) {
+      const uint32_t off = (k >> 2) * (SLAB >> 4) + (k & 3) * 2;
+      tc_mma_f16(d, ((uint64_t)hi << 32) | (a + off), ((uint64_t)hi << 32) | (b + off), idesc, k > 0 ? 1u : 0u);
+    }
+  }
+  __syncwarp();
+}
+// O (+)= P V for 64 keys: P from TMEM, V MN-major, 4 k-steps of 16 keys.
+__device__ __forceinline__ void pack_mma_pv(uint32_t d, uint32_t p, uint32_t b, uint32_t hi, uint32_t idesc, uint32_t acc) {
+  if (pack_elect()) {
+#pragma unroll
+    for (int k = 0; k < TH / 16; ++k)
+      tc_mma_f16_ts(d, p + 8 * k, ((uint64_t)hi << 32) | (b + k * (2048 >> 4)), idesc, k > 0 ? 1u : acc);
+  }
+  __syncwarp();
+}
+__device__ __forceinline__ void pack_arrive(uint64_t* bar) {
+  if (pack_elect()) mbar_arrive(bar);
+  __syncwarp();
+}
+__device__ __forceinline__ void pack_commit(uint64_t* bar) {
+  if (pack_elect()) tc_commit(bar);
+  __syncwarp();
 }
 
 template <int D>
@@ -106,6 +143,8 @@ packed_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
   pdl_prologue();
   using L = PackSmem<D>;
   constexpr int DS = L::DS, NST = L::NST;
+  // of 16 pairs of weights, those whose exponentials are polynomials (see the measurements above)
+  constexpr int POLY = D == 64 ? 5 : 0;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint64_t* bars = reinterpret_cast<uint64_t*>(sm + L::BAR_OFF);
@@ -117,8 +156,10 @@ packed_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
   if (tid == 0) {
     for (int i = 0; i < L::NBAR; ++i) {
       uint32_t cnt = 1;
-      if (i == L::PFULL || i == L::PFULL + 1) cnt = 4;
-      if (i >= L::ITEMFREE && i < L::ITEMFREE + NITEM) cnt = 10;  // 8 softmax warps, the cleaner, the MMA thread
+      if (i >= L::PFULL && i < L::PFULL + 4) cnt = 4;
+      if (i >= L::EMPTY || i == L::QEMPTY) cnt = 2;               // both MMA warps
+      if (i >= L::ITEMFREE && i < L::ITEMFREE + NITEM) cnt = 10 + CLEAN_WARPS;  // softmax, MMA and cleaning warps
+      if (i >= L::VFIX && i < L::VFIX + NFIX) cnt = CLEAN_WARPS;
       mbar_init(&bars[i], cnt);
     }
     fence_barrier_init();
@@ -184,7 +225,7 @@ packed_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
         PackItem* item = &items[slot];
         if (it >= NITEM) {
           int w = 1;
-          if (lane == 0) w = mbar_wait_ool(&bars[L::ITEMFREE + slot], (it / NITEM - 1) & 1, limit, a.status, DETAIL_WAIT_EMPTY, abort_flag, true);
+          if (lane == 0) w = serve_wait(&bars[L::ITEMFREE + slot], (it / NITEM - 1) & 1, limit, a.status, DETAIL_WAIT_EMPTY, abort_flag);
           if (!__shfl_sync(0xffffffffu, w, 0)) break;
         }
         if (end) {
@@ -204,6 +245,8 @@ packed_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
           w.start = start;
           w.len = len;
 #pragma unroll
+          for (int x = 0; x < 8; ++x) w.bad[x >> 2][x & 3] = 0;
+#pragma unroll
           for (int x = 0; x < 2; ++x) {
             const int tile = by_heads ? local : 2 * local + x;
             w.h[x] = by_heads ? 2 * pair + x : pair;
@@ -214,7 +257,7 @@ packed_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
           const int h0 = w.h[0], h1 = w.h[1], r0 = w.row0[0], r1 = w.row0[1], n1 = w.n[1];
           mbar_arrive(&bars[L::ITEMFULL + slot]);
           const int kvh = h0 / a.G;
-          if (it > 0) ok = mbar_wait_ool(&bars[L::QEMPTY], (it - 1) & 1, limit, a.status, DETAIL_WAIT_Q, abort_flag, true);
+          if (it > 0) ok = serve_wait(&bars[L::QEMPTY], (it - 1) & 1, limit, a.status, DETAIL_WAIT_Q, abort_flag);
           for (int t = -1; ok && t < 2 * n; ++t) {
             if (t < 0) {
               mbar_arrive_expect_tx(&bars[L::QFULL], (n1 > 0 ? 2 : 1) * L::STAGE);
@@ -226,7 +269,7 @@ packed_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
               continue;
             }
             const uint32_t st = gs % NST, ph = gs / NST;
-            if (ph > 0 && !mbar_wait_ool(&bars[L::EMPTY + st], (ph - 1) & 1, limit, a.status, DETAIL_WAIT_EMPTY, abort_flag, true)) {
+            if (ph > 0 && !serve_wait(&bars[L::EMPTY + st], (ph - 1) & 1, limit, a.status, DETAIL_WAIT_EMPTY, abort_flag)) {
               ok = false;
               break;
             }
@@ -245,123 +288,176 @@ packed_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
         for (uint32_t g = gs > NST ? gs - NST : 0; g < gs; ++g) serve_drain(&bars[L::FULL + g % NST], (g / NST) & 1);
       }
       __syncwarp();
-    } else if (warp == 9) {
-      // ---------------------------------------------------------- MMA issuer
-      if (lane == 0) {
-        constexpr uint32_t IDESC_QK = idesc_bf16(TM, TN, 0, 0);
-        constexpr uint32_t IDESC_PV = idesc_bf16(TM, D, 0, 1);
-        const uint64_t q_desc = smem_desc(smem_u32(sm + L::Q_OFF), 16, 1024, SWZ_128B);
-        const uint64_t k_desc = smem_desc(smem_u32(sm + L::KV_OFF), 16, 1024, SWZ_128B);
-        const uint64_t v_desc = smem_desc(smem_u32(sm + L::KV_OFF), SLAB, 1024, SWZ_128B);
-        constexpr uint64_t STG = L::STAGE >> 4;
-        uint32_t gs = 0;
-        uint32_t np[2] = {0, 0};  // P tiles consumed so far
-        uint32_t nfix = 0;
-        bool ok = true;
-        for (int it = 0; ok; ++it) {
-          const int slot = it % NITEM;
-          if (!mbar_wait_ool(&bars[L::ITEMFULL + slot], (it / NITEM) & 1, limit, a.status, DETAIL_WAIT_Q, abort_flag, true)) break;
-          const PackItem* im = &items[slot];
-          if (im->start < 0) break;
-          const int n0 = im->n[0], n1 = im->n[1];
-          mbar_arrive(&bars[L::ITEMFREE + slot]);
-          const int n = max(n0, n1);
-          if (!mbar_wait_ool(&bars[L::QFULL], it & 1, limit, a.status, DETAIL_WAIT_Q, abort_flag, true)) break;
-          // step t: P(t-1) V(t-1) of each tile, followed by its S(t)
-          for (int t = 0; ok && t <= n; ++t) {
-            const uint32_t kst = (gs + 2 * t) % NST, kph = ((gs + 2 * t) / NST) & 1;
-            const uint32_t vg = gs + 2 * t - 1;
-            const uint32_t vst = vg % NST, vph = (vg / NST) & 1;
-            bool k_seen = false;
-#pragma unroll
-            for (int x = 0; x < 2; ++x) {
-              const int nx = x ? n1 : n0;
-              if (ok && t > 0 && t - 1 < nx) {
-                ok = mbar_wait_ool(&bars[L::PFULL + x], np[x] & 1, limit, a.status, DETAIL_WAIT_P, abort_flag, true);
-                ++np[x];
-                if (ok && t - 1 >= n0 - 1 && (x == 0 || t - 1 >= n0)) {  // first use of a cleaned V tile
-                  ok = mbar_wait_ool(&bars[L::VFIX], nfix & 1, limit, a.status, DETAIL_WAIT_V, abort_flag, true);
-                  ++nfix;
-                }
-                ok = ok && mbar_wait_ool(&bars[L::FULL + vst], vph, limit, a.status, DETAIL_WAIT_V, abort_flag, true);
-                if (!ok) break;
-                tc_fence_after();
-                pack_mma_pv(tmem + PACK_O + 128 * x, tmem + 128 * x, v_desc + vst * STG, IDESC_PV, t > 1 ? 1u : 0u);
-                tc_commit(&bars[L::ODONE + x]);
+    } else if (warp < 11) {
+      // ---------------------------------------------------------- MMA issuers
+      const int x = __shfl_sync(0xffffffffu, warp, 0) - 9;  // the row tile
+      constexpr uint32_t IDESC_QK = idesc_bf16(TM, TH, 0, 0);
+      constexpr uint32_t IDESC_PV = idesc_bf16(TM, D, 0, 1);
+      const uint64_t q_desc = smem_desc(smem_u32(sm + L::Q_OFF), 16, 1024, SWZ_128B);
+      const uint64_t k_desc = smem_desc(smem_u32(sm + L::KV_OFF), 16, 1024, SWZ_128B);
+      const uint64_t v_desc = smem_desc(smem_u32(sm + L::KV_OFF), SLAB, 1024, SWZ_128B);
+      constexpr uint32_t STG = L::STAGE >> 4;
+      const uint32_t q_lo = __shfl_sync(0xffffffffu, (uint32_t)q_desc, 0) + x * STG;
+      const uint32_t k_lo = __shfl_sync(0xffffffffu, (uint32_t)k_desc, 0), v_lo = __shfl_sync(0xffffffffu, (uint32_t)v_desc, 0);
+      const uint32_t qk_hi = (uint32_t)(q_desc >> 32), pv_hi = (uint32_t)(v_desc >> 32);
+      const uint32_t tm_s = __shfl_sync(0xffffffffu, tmem, 0) + 128 * x, tm_o = tm_s + PACK_O;
+      uint64_t* const pfull = &bars[L::PFULL + 2 * x];
+      uint64_t* const sfull = &bars[L::SFULL + 2 * x];
+      uint32_t gs = 0;     // ring stages of the items before this one
+      uint32_t np = 0;     // key tiles of this row tile whose P has been taken
+      uint32_t nfix = 0;   // V tiles cleaned so far
+      int pt = -1;         // the key tile whose P V comes next (-1: none),
+      bool p_mine = false, p_fix = false;  // whether this row tile has it, whether its V is cleaned,
+      uint32_t pg = 0;     // and the ring place of its V
+      bool ok = true;
+      // Both warps wait for every load and cleaned tile, used or not: that keeps their phases within a ring turn.
+      for (int it = 0; ok; ++it) {
+        const int slot = it % NITEM;
+        if (!serve_warp_wait(&bars[L::ITEMFULL + slot], (it / NITEM) & 1, limit, a.status, DETAIL_WAIT_Q, abort_flag)) break;
+        const PackItem* im = &items[slot];
+        const bool last = __shfl_sync(0xffffffffu, im->start, 0) < 0;
+        const int n0 = __shfl_sync(0xffffffffu, last ? 0 : im->n[0], 0), n1 = __shfl_sync(0xffffffffu, last ? 0 : im->n[1], 0);
+        if (!last) pack_arrive(&bars[L::ITEMFREE + slot]);
+        const int n = max(n0, n1), nx = x ? n1 : n0;
+        // Step t: for each half, P V of the key tile before, then S of tile t.  At t = 0 the tile before is the previous
+        // item's last one; both its halves go first, because this item's Q may still be on its way.
+        for (int t = 0; t < n || (last && t == 0); ++t) {
+          const uint32_t kst = (gs + 2 * t) % NST, kph = ((gs + 2 * t) / NST) & 1;
+          const uint32_t vst = pg % NST, vph = (pg / NST) & 1;
+          auto put_pv = [&](int h) {
+            if (h == 0) {
+              if (p_fix) {
+                ok = serve_warp_wait(&bars[L::VFIX + nfix % NFIX], (nfix / NFIX) & 1, limit, a.status, DETAIL_WAIT_V, abort_flag, true);
+                ++nfix;
               }
-              if (ok && t < nx) {
-                if (!k_seen) ok = mbar_wait_ool(&bars[L::FULL + kst], kph, limit, a.status, DETAIL_WAIT_K, abort_flag, true);
-                k_seen = true;
-                if (!ok) break;
+              ok = ok && serve_warp_wait(&bars[L::FULL + vst], vph, limit, a.status, DETAIL_WAIT_V, abort_flag, true);
+            }
+            if (ok && p_mine) {
+              ok = serve_warp_wait(pfull + h, np & 1, limit, a.status, DETAIL_WAIT_P, abort_flag, true);
+              if (ok) {
                 tc_fence_after();
-                pack_mma_qk<D>(tmem + 128 * x, q_desc + x * STG, k_desc + kst * STG, IDESC_QK);
-                tc_commit(&bars[L::SFULL + x]);
+                pack_mma_pv(tm_o, tm_s + TH * h, v_lo + vst * STG + h * (TH / 16) * (2048 >> 4), pv_hi, IDESC_PV, h > 0 || pt > 0 ? 1u : 0u);
+                pack_commit(&bars[L::ODONE + 2 * x + h]);
               }
             }
-            if (!ok) break;
-            if (t > 0) tc_commit(&bars[L::EMPTY + vst]);
-            if (t < n) tc_commit(&bars[L::EMPTY + kst]);
-            if (t == n - 1) tc_commit(&bars[L::QEMPTY]);
-            if (t < n && t >= n0 - 1) {
-              // the cleaner starts on V(t) while S(t) is in its softmax
-              const uint32_t fg = gs + 2 * t + 1;
-              ok = mbar_wait_ool(&bars[L::FULL + fg % NST], (fg / NST) & 1, limit, a.status, DETAIL_WAIT_V, abort_flag, true);
-              if (ok) mbar_arrive(&bars[L::FIXREQ]);
+          };
+          auto put_qk = [&](int h) {
+            if (h == 0) {
+              ok = serve_warp_wait(&bars[L::FULL + kst], kph, limit, a.status, DETAIL_WAIT_K, abort_flag, true);
+              tc_fence_after();
+            }
+            if (ok && t < nx) {
+              pack_mma_qk<D>(tm_s + TH * h, q_lo, k_lo + kst * STG + h * ((TH * 128) >> 4), qk_hi, IDESC_QK);
+              pack_commit(sfull + h);
+            }
+          };
+          if (t > 0) {
+            put_pv(0);
+            if (ok) put_qk(0);
+            if (ok) put_pv(1);
+            if (ok) put_qk(1);
+          } else {
+            if (pt >= 0) {
+              put_pv(0);
+              if (ok) put_pv(1);
+            }
+            if (ok && n > 0) {
+              ok = serve_warp_wait(&bars[L::QFULL], it & 1, limit, a.status, DETAIL_WAIT_Q, abort_flag, true);
+              if (ok) put_qk(0);
+              if (ok) put_qk(1);
             }
           }
-          gs += 2 * n;
+          if (!ok) break;
+          if (pt >= 0) {
+            np += p_mine ? 1 : 0;
+            pack_commit(&bars[L::EMPTY + vst]);
+          }
+          pt = -1;
+          if (t < n) {
+            pack_commit(&bars[L::EMPTY + kst]);
+            if (t == n - 1) pack_commit(&bars[L::QEMPTY]);
+            pt = t;
+            p_mine = t < nx;
+            p_fix = t >= n0 - 1;
+            pg = gs + 2 * t + 1;
+          }
         }
-        // every MMA issued has finished before TMEM is released (also after an abort)
-        tc_commit(&bars[L::DRAIN]);
-        serve_drain(&bars[L::DRAIN], 0);
+        if (last) break;
+        gs += 2 * n;
       }
+      // every MMA issued has finished before TMEM is released (also after an abort)
+      pack_commit(&bars[L::DRAIN + x]);
+      if (lane == 0) serve_drain(&bars[L::DRAIN + x], 0);
       __syncwarp();
     } else {
       // ---------------------------------------------------------- V cleaner
-      uint32_t gs = 0, nfix = 0;
+      uint32_t gs = 0, nfix = 0, nsec = 0;
       bool ok = true;
       for (int it = 0; ok; ++it) {
         const int slot = it % NITEM;
-        if (!serve_warp_wait(&bars[L::ITEMFULL + slot], (it / NITEM) & 1, limit, a.status, DETAIL_WAIT_Q, abort_flag, true)) break;
+        if (!serve_warp_wait(&bars[L::ITEMFULL + slot], (it / NITEM) & 1, limit, a.status, DETAIL_WAIT_Q, abort_flag)) break;
         PackItem* im = &items[slot];
         if (im->start < 0) break;
         const int n0 = im->n[0], n = max(n0, im->n[1]), len = im->len;
-        if (lane < 8) im->bad[lane >> 2][lane & 3] = 0;
-        __syncwarp();
         for (int t = n0 - 1; t < n; ++t) {
-          if (!serve_warp_wait(&bars[L::FIXREQ], nfix & 1, limit, a.status, DETAIL_WAIT_V, abort_flag, true)) ok = false;
-          ++nfix;
+          // asked for by the softmax that meets the tile; by then the stage's use before this one is known to be over
+          const uint32_t g = gs + 2 * t + 1, st = g % NST;
+          const int second = t - (n0 - 1);
+          ok = serve_warp_wait(&bars[L::FIXREQ + second], (second ? nsec++ : (uint32_t)it) & 1, limit, a.status, DETAIL_WAIT_V, abort_flag) &&
+               serve_warp_wait(&bars[L::FULL + st], (g / NST) & 1, limit, a.status, DETAIL_WAIT_V, abort_flag);
+          bool wrote = false;
           if (ok) {
-            const uint32_t st = (gs + 2 * t + 1) % NST;
             uint8_t* v = sm + L::KV_OFF + st * L::STAGE;
             const int live = len - t * TN;  // rows from here on are behind the sequence
+            const int w0 = warp - 11;       // 16-byte pieces i * 32 + lane, i of this warp: 4 rows each
 #pragma unroll 1
-            for (int i0 = 0; i0 < DS * 32; i0 += 8) {
+            for (int i0 = w0 * 8; i0 < DS * 32; i0 += 8 * CLEAN_WARPS) {
               uint4 w[8];
 #pragma unroll
               for (int q = 0; q < 8; ++q) w[q] = *reinterpret_cast<const uint4*>(v + ((i0 + q) * 32 + lane) * 16);
+              if (live < TN) {
 #pragma unroll
-              for (int q = 0; q < 8; ++q) {
-                const int row = (((i0 + q) * 32 + lane) >> 3) & 127;
-                if (row >= live) {
-                  *reinterpret_cast<uint4*>(v + ((i0 + q) * 32 + lane) * 16) = make_uint4(0, 0, 0, 0);
-                } else {
-                  // a half whose exponent is all ones carries into its top bit
-                  const uint32_t hit = (((w[q].x & 0x7f807f80u) + 0x00800080u) | ((w[q].y & 0x7f807f80u) + 0x00800080u) |
-                                        ((w[q].z & 0x7f807f80u) + 0x00800080u) | ((w[q].w & 0x7f807f80u) + 0x00800080u)) & 0x80008000u;
-                  if (hit) {
-                    uint16_t* e = reinterpret_cast<uint16_t*>(v + ((i0 + q) * 32 + lane) * 16);
-                    for (int j = 0; j < 8; ++j)
-                      if ((e[j] & 0x7f80u) == 0x7f80u) e[j] = 0;
-                    atomicOr(&im->bad[t - (n0 - 1)][row >> 5], 1u << (row & 31));
+                for (int q = 0; q < 8; ++q) {
+                  if ((((i0 + q) * 4 + (lane >> 3)) & 127) >= live) {
+                    *reinterpret_cast<uint4*>(v + ((i0 + q) * 32 + lane) * 16) = w[q] = make_uint4(0, 0, 0, 0);
+                    wrote = true;
                   }
                 }
               }
+              // 0 x is 0, or NaN where x is not finite
+              const __nv_bfloat162 zero = __floats2bfloat162_rn(0.f, 0.f);
+              __nv_bfloat162 acc[4] = {zero, zero, zero, zero};
+#pragma unroll
+              for (int q = 0; q < 8; ++q) {
+                acc[0] = __hfma2(*reinterpret_cast<const __nv_bfloat162*>(&w[q].x), zero, acc[0]);
+                acc[1] = __hfma2(*reinterpret_cast<const __nv_bfloat162*>(&w[q].y), zero, acc[1]);
+                acc[2] = __hfma2(*reinterpret_cast<const __nv_bfloat162*>(&w[q].z), zero, acc[2]);
+                acc[3] = __hfma2(*reinterpret_cast<const __nv_bfloat162*>(&w[q].w), zero, acc[3]);
+              }
+              acc[0] = __hadd2(__hadd2(acc[0], acc[1]), __hadd2(acc[2], acc[3]));
+              const float seen = __low2float(acc[0]) + __high2float(acc[0]);
+              if (seen != seen) {
+                wrote = true;
+#pragma unroll 1
+                for (int q = 0; q < 8; ++q) {
+                  uint16_t* e = reinterpret_cast<uint16_t*>(v + ((i0 + q) * 32 + lane) * 16);
+                  const int row = ((i0 + q) * 4 + (lane >> 3)) & 127;
+                  bool hit = false;
+                  for (int j = 0; j < 8; ++j) {
+                    if ((e[j] & 0x7f80u) == 0x7f80u) {
+                      e[j] = 0;
+                      hit = true;
+                    }
+                  }
+                  if (hit) atomicOr(&im->bad[t - (n0 - 1)][row >> 5], 1u << (row & 31));
+                }
+              }
             }
-            fence_proxy_async_smem();
+            if (wrote) fence_proxy_async_smem();  // (a fence holds back the arrival below by some 1000 cycles)
           }
           __syncwarp();
-          if (ok && lane == 0) mbar_arrive(&bars[L::VFIX]);
+          if (ok && lane == 0) mbar_arrive(&bars[L::VFIX + nfix % NFIX]);
+          ++nfix;
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(&bars[L::ITEMFREE + slot]);
@@ -375,7 +471,7 @@ packed_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
     const int r = q4 * 32 + lane;  // row of the tile == TMEM lane
     const uint32_t s_t = tmem + ((uint32_t)(q4 * 32) << 16) + 128 * x;
     const uint32_t o_t = s_t + PACK_O;
-    uint32_t ns = 0;  // S tiles seen so far
+    uint32_t ns = 0;  // halves of S tiles seen so far
     bool ok = true;
     for (int it = 0; ok; ++it) {
       const int slot = it % NITEM;
@@ -385,21 +481,26 @@ packed_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
       const int n = im->n[x], start = im->start, row = im->row0[x] + r, h = im->h[x];
       const bool in = n > 0 && row < im->len;
       float m = -INFINITY, l = 0.f;
-      for (int t = 0; t < n; ++t) {
-        if (!serve_warp_wait_inline(&bars[L::SFULL + x], ns & 1, limit, a.status, DETAIL_WAIT_S, abort_flag)) { ok = false; break; }
+#pragma unroll 1
+      for (int u = 0; u < 2 * n; ++u) {
+        const int half = u & 1;
+        const uint32_t s_h = s_t + TH * half;
+        if (!serve_warp_wait_inline(&bars[L::SFULL + 2 * x + half], (ns >> 1) & 1, limit, a.status, DETAIL_WAIT_S, abort_flag)) { ok = false; break; }
         ++ns;
         tc_fence_after();
-        float s[128];
-#pragma unroll
-        for (int c = 0; c < 4; ++c) tmem_ld32(s_t + 32 * c, s + 32 * c);
+        float s[TH];
+        tmem_ld32(s_h, s);
+        tmem_ld32(s_h + 32, s + 32);
         tmem_wait_ld();
-        if (t == n - 1) {  // the tile on the diagonal
+        if (u >= 2 * n - 2) {  // the tile on the diagonal
+          if (half == 0 && warp == 4 * x && lane == 0 && (x == 0 || n > im->n[0])) mbar_arrive(&bars[L::FIXREQ + x]);  // its V may be cleaned
+          const int seen = r - TH * half;
 #pragma unroll
-          for (int c = 0; c < 128; ++c) s[c] = c <= r ? s[c] : -INFINITY;
+          for (int c = 0; c < TH; ++c) s[c] = c <= seen ? s[c] : -INFINITY;
         }
         float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-        for (int c = 0; c < 64; ++c) mx[c & 3] = serve_max3(mx[c & 3], s[2 * c], s[2 * c + 1]);
+        for (int c = 0; c < TH / 2; ++c) mx[c & 3] = serve_max3(mx[c & 3], s[2 * c], s[2 * c + 1]);
         const float m_new = fmaxf(m, fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * a.scale_log2);
         float alpha = 1.f;
         bool need = false;
@@ -411,8 +512,9 @@ packed_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
           }
           m = m_new;
         }
-        if (t > 0 && __any_sync(0xffffffffu, need)) {
-          if (!serve_warp_wait_inline(&bars[L::ODONE + x], (ns - 2) & 1, limit, a.status, DETAIL_WAIT_O, abort_flag)) { ok = false; break; }
+        if (u > 0 && __any_sync(0xffffffffu, need)) {
+          // P V of the half before: the only one that can be under way
+          if (!serve_warp_wait_inline(&bars[L::ODONE + 2 * x + (half ^ 1)], ((ns - 2) >> 1) & 1, limit, a.status, DETAIL_WAIT_O, abort_flag)) { ok = false; break; }
           tc_fence_after();
 #pragma unroll 1
           for (int c = 0; c < D / 16; ++c) {
@@ -427,32 +529,37 @@ packed_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
         const float negm = (m == -INFINITY) ? 0.f : -m;
         float ls[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
+        for (int c = 0; c < TH / 32; ++c) {
           uint32_t pk[16];
 #pragma unroll
           for (int i = 0; i < 16; ++i) {
             float x0, x1;
             serve_fma2(s[32 * c + 2 * i], s[32 * c + 2 * i + 1], a.scale_log2, negm, x0, x1);
-            const float p0 = serve_ex2(x0), p1 = serve_ex2(x1);
+            float p0, p1;
+            if (i < POLY) {
+              serve_ex2_poly2(x0, x1, p0, p1);
+            } else {
+              p0 = serve_ex2(x0);
+              p1 = serve_ex2(x1);
+            }
             serve_add2(ls[(i & 1) * 2], ls[(i & 1) * 2 + 1], p0, p1);
             __nv_bfloat162 v2 = __floats2bfloat162_rn(p0, p1);
             pk[i] = *reinterpret_cast<uint32_t*>(&v2);
           }
-          serve_tmem_st16(s_t + 16 * c, pk);
+          serve_tmem_st16(s_h + 16 * c, pk);
         }
         l += (ls[0] + ls[1]) + (ls[2] + ls[3]);
         tmem_wait_st();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&bars[L::PFULL + x]);
+        if (lane == 0) mbar_arrive(&bars[L::PFULL + 2 * x + half]);
       }
       if (!ok) break;
       if (n > 0) {
-        if (!serve_warp_wait_inline(&bars[L::ODONE + x], (ns - 1) & 1, limit, a.status, DETAIL_WAIT_O, abort_flag)) break;
+        if (!serve_warp_wait_inline(&bars[L::ODONE + 2 * x + 1], ((ns >> 1) - 1) & 1, limit, a.status, DETAIL_WAIT_O, abort_flag)) break;
         tc_fence_after();
         const float inv = (l > 0.f) ? 1.f / l : (l == 0.f ? 0.f : l);  // l is 0 without a key of weight, NaN stays
         const int64_t grow = (int64_t)start + (in ? row : 0);
-        __nv_bfloat16* orow = a.O + (int64_t)h * a.o_hs + grow * a.o_ts;
         // cleaned key tiles that this tile's rows see: the diagonal one, and tile A's diagonal one in front of it
         const int first_bad = im->n[0] - 1;
         uint32_t any_bad = 0;
@@ -460,6 +567,7 @@ packed_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
           const uint32_t* bad = im->bad[i - first_bad];
           any_bad |= bad[0] | bad[1] | bad[2] | bad[3];
         }
+        __nv_bfloat16* orow = a.O + (int64_t)h * a.o_hs + grow * a.o_ts;
 #pragma unroll 1
         for (int c = 0; c < D / 32; ++c) {
           float o[32];
@@ -481,6 +589,7 @@ packed_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
               }
             }
           }
+          // (rows by way of shared memory, so that a store writes whole lines: no faster)
           if (in) {
             uint32_t pk[16];
 #pragma unroll

@@ -82,12 +82,34 @@ static __device__ __noinline__ void serve_drain(uint64_t* bar, uint32_t parity) 
   }
 }
 
+// Waits for a phase, bounded like mbar_wait.  With `poll` the thread keeps asking; without it, the hardware
+// suspends it, which leaves the issue slots to others but wakes it some hundred cycles later.
+static __device__ __noinline__ bool serve_wait_loop(uint64_t* bar, uint32_t parity, uint64_t limit, unsigned* status,
+                                                    unsigned detail, volatile int* abort_flag, bool poll) {
+  const uint64_t t0 = globaltimer_ns();
+  uint32_t spins = 0;
+  while (true) {
+    if (poll ? mbar_test_wait(bar, parity) : mbar_try_wait(bar, parity)) return true;
+    if (((++spins) & 31u) == 0u) {
+      if (*abort_flag) return false;
+      if (globaltimer_ns() - t0 > limit) {
+        report_timeout(status, detail, abort_flag);
+        return false;
+      }
+    }
+  }
+}
+__device__ __forceinline__ bool serve_wait(uint64_t* bar, uint32_t parity, uint64_t limit, unsigned* status, unsigned detail,
+                                           volatile int* abort_flag, bool poll = false) {
+  if (mbar_test_wait(bar, parity)) return true;
+  return serve_wait_loop(bar, parity, limit, status, detail, abort_flag, poll);
+}
 // One lane waits, the whole warp learns the outcome.
 __device__ __forceinline__ bool serve_warp_wait(uint64_t* bar, uint32_t parity, uint64_t limit, unsigned* status,
-                                                unsigned detail, volatile int* abort_flag, bool suspend) {
-  if (__all_sync(0xffffffffu, mbar_test_wait(bar, parity))) return true;
+                                                unsigned detail, volatile int* abort_flag, bool poll = false) {
+  if (__builtin_expect(__all_sync(0xffffffffu, mbar_test_wait(bar, parity)), 1)) return true;
   int ok = 0;
-  if ((threadIdx.x & 31) == 0) ok = mbar_wait_ool(bar, parity, limit, status, detail, abort_flag, suspend) ? 1 : 0;
+  if ((threadIdx.x & 31) == 0) ok = serve_wait_loop(bar, parity, limit, status, detail, abort_flag, poll) ? 1 : 0;
   ok = __shfl_sync(0xffffffffu, ok, 0);
   __syncwarp();
   return ok != 0;
@@ -139,6 +161,16 @@ __device__ __forceinline__ void serve_fma2(float a0, float a1, float b, float c,
   asm("mov.b64 {%0, %1}, %2;" : "=f"(x0), "=f"(x1) : "l"(r));
 }
 
+// (x0, x1) = (a0, a1) * (b0, b1) + (c0, c1) as one packed multiply-add
+__device__ __forceinline__ void serve_fma2v(float a0, float a1, float b0, float b1, float c0, float c1, float& x0, float& x1) {
+  uint64_t av, bv, cv, r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(av) : "f"(a0), "f"(a1));
+  asm("mov.b64 %0, {%1, %2};" : "=l"(bv) : "f"(b0), "f"(b1));
+  asm("mov.b64 %0, {%1, %2};" : "=l"(cv) : "f"(c0), "f"(c1));
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(av), "l"(bv), "l"(cv));
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(x0), "=f"(x1) : "l"(r));
+}
+
 // (s0, s1) += (a, b) as one packed add
 __device__ __forceinline__ void serve_add2(float& s0, float& s1, float a, float b) {
   uint64_t sv, av;
@@ -146,6 +178,28 @@ __device__ __forceinline__ void serve_add2(float& s0, float& s1, float a, float 
   asm("mov.b64 %0, {%1, %2};" : "=l"(av) : "f"(a), "f"(b));
   asm("add.rn.f32x2 %0, %0, %1;" : "+l"(sv) : "l"(av));
   asm("mov.b64 {%0, %1}, %2;" : "=f"(s0), "=f"(s1) : "l"(sv));
+}
+
+// (2^x0, 2^x1) on the multiply-add pipe, for x <= 100: 2^x = 2^n 2^f with n the nearest integer and a polynomial of
+// degree 5 in f (|f| <= 1/2, fitted for the smallest largest relative error, 7.5e-8; 2.1e-7 with its roundings).
+// Below -127 the result is 0, for -infinity too; NaN stays NaN.
+__device__ __forceinline__ void serve_ex2_poly2(float x0, float x1, float& p0, float& p1) {
+  asm("max.NaN.f32 %0, %0, 0fC2FE0000;" : "+f"(x0));  // -127
+  asm("max.NaN.f32 %0, %0, 0fC2FE0000;" : "+f"(x1));
+  constexpr float kRound = 12582912.f;  // 1.5 * 2^23: the sum's low bits are n
+  float t0 = kRound, t1 = kRound, r0, r1, f0, f1;
+  serve_add2(t0, t1, x0, x1);
+  r0 = t0;
+  r1 = t1;
+  serve_add2(r0, r1, -kRound, -kRound);
+  serve_fma2v(r0, r1, -1.f, -1.f, x0, x1, f0, f1);
+  float y0 = 0.0013276472454890609f, y1 = y0;
+  constexpr float c[5] = {1.0000001192092896f, 0.6931469440460205f, 0.24022120237350464f, 0.05550713092088699f, 0.009675540961325169f};
+#pragma unroll
+  for (int i = 4; i >= 0; --i) serve_fma2v(y0, y1, f0, f1, c[i], c[i], y0, y1);
+  const float s0 = __int_as_float((__float_as_int(t0) << 23) + 0x3f800000);
+  const float s1 = __int_as_float((__float_as_int(t1) << 23) + 0x3f800000);
+  serve_fma2v(y0, y1, s0, s1, 0.f, 0.f, p0, p1);
 }
 
 // 16 consecutive 32-bit columns of this thread's TMEM lane

@@ -53,6 +53,8 @@ CASES = [
     (1, 1, 64, [1]), (2, 1, 128, [1, 1, 1]), (2, 1, 128, [127]), (2, 2, 128, [128]), (4, 2, 64, [129]),
     (1, 1, 128, [255, 256, 257]), (3, 1, 64, [128, 384, 5, 640]), (6, 2, 128, [700, 3, 129]),
     (4, 2, 64, [1, 2, 130, 0, 500, 0]), (5, 5, 128, [300]), (8, 1, 128, [1000, 257, 1]), (16, 2, 64, [2049]),
+    # long sequences of odd head groups: row tiles of different lengths walk the keys together
+    (3, 1, 64, [5000]), (2, 2, 64, [4096, 1, 3000]), (1, 1, 128, [3500, 129]),
 ]
 
 
