@@ -246,6 +246,15 @@ __device__ __forceinline__ uint32_t rescale_e4m3x4(uint32_t x, float f) {
 __device__ __forceinline__ float pow2f(int e) { return __int_as_float((e + 127) << 23); }
 __device__ __forceinline__ bool good_scale(float s) { return s >= 5.42101086e-20f && s <= 1.84467441e19f; }  // 2^-64 .. 2^64
 
+// The first set bit at or behind `from` in ST_THREADS bits, or -1.
+__device__ __forceinline__ int next_bit(const uint32_t* bits, int from) {
+  for (int i = from >> 5; i < ST_THREADS / 32; ++i) {
+    const uint32_t w = i == from >> 5 ? bits[i] & (~0u << (from & 31)) : bits[i];
+    if (w != 0) return i * 32 + __ffs(w) - 1;
+  }
+  return -1;
+}
+
 template <int D>
 __global__ void __launch_bounds__(ST_THREADS) k_cache_store(const __grid_constant__ StoreArgs a) {
   pdl_prologue();
@@ -253,21 +262,30 @@ __global__ void __launch_bounds__(ST_THREADS) k_cache_store(const __grid_constan
   constexpr int RPP = ST_THREADS / LPR;        // rows of a pass
   __shared__ int s_end[ST_THREADS / 32];
   __shared__ uint32_t s_max[ST_THREADS / 32];
+  __shared__ uint32_t s_starts[ST_THREADS / 32];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int h = blockIdx.y, kv = blockIdx.z;
   const int page = 1 << a.shift;
   const int64_t slots_end = (int64_t)a.num_pages << a.shift;
-  const int c0 = blockIdx.x * a.chunk, c1 = min(a.T, c0 + a.chunk);
   const int sub = tid % LPR, r0 = tid / LPR;
-  for (int t = c0; t < c1; ++t) {
-    const int slot = a.slots[t];
-    if (slot < 0) continue;
-    const int off = slot & (page - 1);
-    if (off > 0 && t > 0 && a.slots[t - 1] == slot - 1) continue;  // inside a run
-    if (slot >= slots_end) {
-      if (tid == 0) report(a.status, DSA_ERR_DEVICE, DETAIL_BAD_SLOT);
-      continue;
+  // the runs that begin among this CTA's tokens (at most as many as threads)
+  const int c0 = blockIdx.x * a.chunk;
+  bool starts = false;
+  if (tid < a.chunk && c0 + tid < a.T) {
+    const int s = a.slots[c0 + tid];
+    starts = s >= 0 && ((s & (page - 1)) == 0 || c0 + tid == 0 || a.slots[c0 + tid - 1] != s - 1);
+    if (starts && s >= slots_end) {
+      report(a.status, DSA_ERR_DEVICE, DETAIL_BAD_SLOT);
+      starts = false;
     }
+  }
+  const uint32_t ballot = __ballot_sync(0xffffffffu, starts);
+  if (lane == 0) s_starts[warp] = ballot;
+  __syncthreads();
+  for (int c = next_bit(s_starts, 0); c >= 0; c = next_bit(s_starts, c + 1)) {
+    const int t = c0 + c;
+    const int slot = a.slots[t];
+    const int off = slot & (page - 1);
     // tokens of the run
     const int most = min(page - off, a.T - t);
     int n = 0;
@@ -1032,7 +1050,10 @@ dsa_status dsa_cache_write(const dsa_cache* cache, const void* K, const void* V,
   a.Hkv = cache->Hkv;
   a.shift = log2_page(cache->page);
   a.num_pages = cache->num_pages;
-  a.chunk = n_tokens <= 4096 ? 1 : 16;
+  // a token a CTA while CTAs are few (each may be a run of its own), up to 128 once there are enough for every SM
+  int chunk = 1;
+  while (chunk < ST_THREADS && (int64_t)n_tokens * cache->Hkv * 2 > (int64_t)chunk * 4096) chunk *= 2;
+  a.chunk = chunk;
   a.status = st;
   const dim3 grid(ceil_div(n_tokens, a.chunk), cache->Hkv, 2);
   cudaError_t e = cache->d == 128 ? launch_pdl(k_cache_store<128>, grid, dim3(ST_THREADS), 0, (cudaStream_t)stream, a)
