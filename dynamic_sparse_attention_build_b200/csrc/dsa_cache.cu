@@ -31,16 +31,17 @@ __device__ __forceinline__ int owner_of(const int* pre, int n, int i) {
 // Page tables.  Released requests (new < 0) push their pages on the free stack; then request b
 // takes ceil((l + n) / P) - ceil(l / P) pages from its top, in request order; token i of request
 // b goes to slot table[b][(l + i) / P] * P + (l + i) % P.
-// Bound by latency: three dependent steps (lengths, pushes, takes) over a few hundred kB at most.
-// One cluster does all of it: every CTA scans all lengths itself (three prefix sums in shared
-// memory), the pushes and takes are flattened over the cluster's threads (one page each, found by
-// binary search), and cluster barriers order what is read before what is written, so lengths and
-// counts may be updated in place.
+// Bound by latency: a few hundred kB at most.  Every CTA scans all lengths itself (three prefix sums in shared
+// memory); pushes, takes and slots are flattened over all threads (one page or four slots each, found by binary
+// search).  Nothing is read that the call writes: a taken page is looked up where it comes from, the old stack or the
+// row of the request that gave it back; pushes go behind the old stack, takes behind a row's old pages.  So no step
+// waits for another, but for one case: where lengths or count are updated in place, one cluster does all the work,
+// and its barrier stands between their reads and writes.
 // ---------------------------------------------------------------------------
 constexpr int TAB_THREADS = 512;
 
 struct TableArgs {
-  int n_req, width, shift, max_tokens, free_cap;
+  int n_req, width, shift, max_tokens, free_cap, in_place;
   const int32_t* lens;
   const int32_t* new_lens;
   int32_t* free_pages;
@@ -133,26 +134,24 @@ __global__ void __launch_bounds__(TAB_THREADS, 1) k_build_tables(const __grid_co
   }
   __syncthreads();
   const int at = rank * TAB_THREADS + tid;
+  // the k-th page taken: from the old stack, or from the row of a request that ends
+  const int freed = (int)total[2];
+  auto taken = [&](int k) {
+    const int i = freed - 1 - k;
+    if (i < 0) return a.free_pages[count + i];
+    const int b = owner_of(give, n, i);
+    return a.table[(int64_t)b * a.width + (i - give[b])];
+  };
   if (ok) {
-    for (int i = at; i < (int)total[2]; i += nthreads) {
+    for (int i = at; i < freed; i += nthreads) {
       const int b = owner_of(give, n, i);
       a.free_pages[count + i] = a.table[(int64_t)b * a.width + (i - give[b])];
     }
-  }
-  // all pushes are visible, and every CTA has read lengths and count
-  if (gridDim.x > 1) cluster_sync(); else __syncthreads();
-  const int top = count + (int)total[2] - 1;
-  if (ok) {
     for (int i = at; i < (int)total[1]; i += nthreads) {
       const int b = owner_of(take, n, i);
-      a.table[(int64_t)b * a.width + ((old[b] + page - 1) >> a.shift) + (i - take[b])] = a.free_pages[top - i];
+      a.table[(int64_t)b * a.width + ((old[b] + page - 1) >> a.shift) + (i - take[b])] = taken(i);
     }
   }
-  for (int i = at; i <= n; i += nthreads) {
-    a.cu[i] = ok ? cu[i] : 0;
-    if (i < n) a.lens_out[i] = ok ? old[i] + (cu[i + 1] - cu[i]) : a.lens[i];
-  }
-  if (at == 0) *a.count_out = ok ? top + 1 - (int)total[1] : count;
   // slots, four tokens a thread; a token's page comes from the stack or, for the page that held
   // its request's last token, from the table
   const int live = ok ? (int)total[0] : 0;
@@ -173,7 +172,7 @@ __global__ void __launch_bounds__(TAB_THREADS, 1) k_build_tables(const __grid_co
         const int pos = old[b] + (t - cu[b]);
         const int j = pos >> a.shift, have = (old[b] + page - 1) >> a.shift;
         if (j != seen) {
-          pg = j < have ? a.table[(int64_t)b * a.width + j] : a.free_pages[top - (take[b] + j - have)];
+          pg = j < have ? a.table[(int64_t)b * a.width + j] : taken(take[b] + j - have);
           seen = j;
           if (pg < 0 || pg > (0x7fffffff >> a.shift)) {  // a table or stack that holds no page here
             report(a.status, DSA_ERR_DEVICE, DETAIL_BAD_PAGE);
@@ -190,6 +189,12 @@ __global__ void __launch_bounds__(TAB_THREADS, 1) k_build_tables(const __grid_co
         if (t0 + k < a.max_tokens) a.slots[t0 + k] = v[k];
     }
   }
+  if (a.in_place && gridDim.x > 1) cluster_sync();  // every CTA has read lengths and count
+  for (int i = at; i <= n; i += nthreads) {
+    a.cu[i] = ok ? cu[i] : 0;
+    if (i < n) a.lens_out[i] = ok ? old[i] + (cu[i + 1] - cu[i]) : a.lens[i];
+  }
+  if (at == 0) *a.count_out = ok ? count + freed - (int)total[1] : count;
 }
 
 // ---------------------------------------------------------------------------
@@ -1009,13 +1014,22 @@ dsa_status dsa_build_tables(int32_t n_req, const int32_t* lens, const int32_t* n
   a.lens_out = lens_out;
   a.count_out = free_count_out;
   a.status = st;
+  // (arrays that overlap in part are not in place, but as safe this way)
+  auto meet = [](const int32_t* x, int64_t nx, const int32_t* y, int64_t ny) { return x < y + ny && y < x + nx; };
+  a.in_place = meet(lens, n_req, lens_out, n_req) || meet(new_lens, n_req, lens_out, n_req) ||
+                       meet(free_count, 1, free_count_out, 1)
+                   ? 1
+                   : 0;
+  const int most = a.in_place ? 8 : 148;
   int ctas = 1;
-  while (ctas < 8 && ctas * TAB_THREADS * 8 < max_tokens) ctas *= 2;
+  while (ctas < most && ctas * TAB_THREADS * 4 < max_tokens) ctas = min(most, ctas * 2);
   const size_t smem = (size_t)(4 * n_req + 3) * 4;
   int dev = 0, sms = 0;
   cudaError_t e = serve_sms(&dev, &sms);
   if (e == cudaSuccess) e = serve_allow_smem<k_build_tables>(dev, (4 * MAX_REQ + 3) * 4);
-  if (e == cudaSuccess) e = serve_launch_cluster(k_build_tables, dim3(ctas), dim3(TAB_THREADS), ctas, smem, (cudaStream_t)stream, a);
+  if (e == cudaSuccess)
+    e = a.in_place && ctas > 1 ? serve_launch_cluster(k_build_tables, dim3(ctas), dim3(TAB_THREADS), ctas, smem, (cudaStream_t)stream, a)
+                               : launch_pdl(k_build_tables, dim3(ctas), dim3(TAB_THREADS), smem, (cudaStream_t)stream, a);
   if (e == cudaSuccess) e = cudaGetLastError();
   return e == cudaSuccess ? DSA_OK : cuda_fail(e);
 }
