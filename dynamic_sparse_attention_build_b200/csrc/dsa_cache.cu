@@ -381,26 +381,36 @@ __global__ void __launch_bounds__(ST_THREADS) k_cache_store(const __grid_constan
 //   O = sum_j softmax_j(q . k_j ks / sqrt(d)) v_j vs,  j <= len - n_q + i for token i,
 // k, v: e4m3 values, ks, vs: their page's scales.
 // Bound by memory: 2 d bytes per key and KV head, read once.  All query heads of a KV head and all
-// n_q tokens are rows of one m16 tile, so each key is converted once; e4m3 is exact in fp16, q is
-// scaled by a power of two per row so that its 8 bits are exact in fp16 too, products accumulate
-// in fp32 (mma m16n8k16; the tensor work is a fraction of what the legacy path carries).
+// n_q tokens are the columns of one n8 tile (or two), so each key is converted once; e4m3 is exact
+// in fp16, q is scaled by a power of two per row so that its 8 bits are exact in fp16 too, products
+// accumulate in fp32.  Keys (and, in the second product, value dimensions) are the m16 side of mma
+// m16n8k16, S^T = K Q^T and O^T = V^T P^T: decoding has few queries, and as the m16 side they would
+// leave three quarters of the products and accumulators empty.  The tensor work is a fraction of what
+// the legacy path carries; tcgen05 would want 128 rows and both operands of 8 bits in one type.
 // Weights: with x = s ks and y = x + log2(vs) (log2 units), P = 2^(y - m + P_OFF) carries the value
 // scale, so pages of any scale share one accumulator, and l sums P / vs.  m lags the running
 // maximum by at most P_LAG: P <= 2^15 in fp16 (11 bits), underflow 2^-34 below the maximum.
 // Split: the work (64-key tiles of all requests, KV heads and row tiles, laid end to end) is
-// cut into equal ranges, one per CTA, three CTAs per SM; so a long request spreads over many CTAs
+// cut into equal ranges, one per CTA, a few CTAs per SM; so a long request spreads over many CTAs
 // and short ones share one.  A CTA's four warps take every fourth 16 keys, each through its own
-// ring of cp.async stages (no barrier in the loop), and join at the end of a unit; units cut by a
-// range's end leave fp32 partials that k_cache_join adds in range order.
+// ring of TMA stages (two boxes of 16 rows, swizzled so that the reads below have no bank conflicts;
+// no barrier between warps in the loop), and join at the end of a unit; units cut by a range's end
+// leave fp32 partials that k_cache_join adds in range order.
 // ---------------------------------------------------------------------------
 constexpr int AT_THREADS = 128;
 constexpr int AT_WARPS = AT_THREADS / 32;
 constexpr int AT_KEYS = 16;                  // keys of a warp's step
 constexpr int AT_TILE = AT_KEYS * AT_WARPS;  // keys of a CTA's step
-constexpr int AT_MAX_CTAS = 444;             // sizes the workspace
-constexpr int AT_PER_SM = 3;
-constexpr int AT_MIN_TILES = 4;              // a CTA takes at least so many tiles
+constexpr int AT_MAX_CTAS = 592;             // sizes the workspace
+// A CTA takes at least so many tiles.  One request of 1000 tokens, 8 KV heads: 10.3 us with 4 (32 CTAs), 12.9 with 3,
+// 14.0 with 6.
+constexpr int AT_MIN_TILES = 4;
 constexpr float P_OFF = 10.f, P_LAG = 5.f;
+// CTAs of an SM, with at_stages() ring stages each: what counts is the bytes on their way.  d 128, a million keys of 8
+// heads: 352 us with 3 CTAs of 4 stages, 409 with 2 of 6, 422 with 4 of 3.  d 64 (boxes half as large), 20 requests
+// of up to 4001 tokens, 16 heads: 37 us with 4 CTAs of 6 stages, 55 with 3 of 8.
+__host__ __device__ constexpr int at_per_sm(int d, int nq) { return d == 64 && nq == 1 ? 4 : 3; }
+__host__ __device__ constexpr int at_stages(int d) { return d == 128 ? 4 : 6; }
 
 struct AttendArgs {
   const __nv_bfloat16* Q;
@@ -419,27 +429,44 @@ struct AttendArgs {
   int n_req, width, Hkv, G, n_q, shift, num_pages, MT, T;
   float scale_log2;
   unsigned* status;
+  uint64_t wait_limit_ns;
 };
 
 template <int D>
 struct AttendSmem {
-  static constexpr int NST = D == 128 ? 4 : 6;
-  static constexpr int STAGE = AT_KEYS * D * 2 + 16;  // K rows, V rows, the two scales
-  static constexpr int RING = AT_WARPS * NST * STAGE;
+  static constexpr int NST = at_stages(D);
+  static constexpr int BOX = AT_KEYS * D;  // 16 rows of K or V
+  static constexpr int RING = AT_WARPS * NST * 2 * BOX;
   static constexpr int JOIN = AT_WARPS * 16 * (D + 4) * 4;
-  static constexpr int PRE = RING > JOIN ? RING : JOIN;
-  static int bytes(int n_req) { return PRE + (n_req + 1) * 4; }
+  static constexpr int SC = RING > JOIN ? RING : JOIN;         // float2 [warp][stage]: the scales, 0: no keys
+  static constexpr int BAR = SC + AT_WARPS * NST * 8;          // uint64 [warp][stage]
+  static constexpr int PRE = BAR + AT_WARPS * NST * 8;         // int [requests + 1]
+  static int bytes(int n_req) { return 1024 + PRE + (n_req + 1) * 4; }
 };
 
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+// Box of 16 rows at (page, head, token) of K or V.
+__device__ __forceinline__ void tma_load_rows(void* dst, const CUtensorMap* map, uint64_t* bar, int token, int head, int page) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(0), "r"(token), "r"(head), "r"(page), "r"(smem_u32(bar))
+      : "memory");
 }
-__device__ __forceinline__ void cp_async4(uint32_t dst, const void* src) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+// Transposes an 8 x 8 matrix of 16-bit values, two a lane.
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
 }
-__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+// The key that row i (0 .. 7) of an m-tile's half stands for.  Any order of the keys will do as long as both products
+// share it; this one keeps 16-byte reads of K (rows i, i + 1 together) and reads of V (rows i, i + 2, ..) free of bank
+// conflicts under the swizzles of 128-byte and of 64-byte rows.
+template <int D>
+__device__ __forceinline__ int key_of(int i) {
+  if (D == 128) return (i & 1) ? (i - 1) ^ 5 : i;
+  const int e = ((i >> 1) & 1) | ((i >> 2) << 2);
+  return (i & 1) ? e ^ 3 : e;
+}
 
 __device__ __forceinline__ void mma_f16(float* c, const uint32_t* a, uint32_t b0, uint32_t b1) {
   asm volatile(
@@ -498,10 +525,23 @@ __device__ __forceinline__ int scan_tiles(const AttendArgs& a, int* pre, bool te
   return base;
 }
 
-// First tile of CTA c's range when `total` tiles are cut over `n` CTAs.
-__device__ __forceinline__ int64_t cut_at(int64_t total, int n, int c) { return total * c / n; }
+// Divisions of 64-bit numbers that nearly always fit 32 bits (a 64-bit division takes some hundred cycles).
+__device__ __forceinline__ int64_t div_by(int64_t x, int64_t y) {
+  return ((x | y) >> 32) == 0 ? (int64_t)((uint32_t)x / (uint32_t)y) : x / y;
+}
+// `total` tiles over n CTAs: the first `rest` get one more than the others.
+struct Cut {
+  int64_t each;
+  int rest;
+  __device__ __forceinline__ Cut(int64_t total, int n) : each(div_by(total, n)), rest((int)(total - each * n)) {}
+  __device__ __forceinline__ int64_t first(int c) const { return c * each + min(c, rest); }  // of CTA c's range
+  __device__ __forceinline__ int holder(int64_t tile) const {                                // the CTA whose range holds it
+    const int64_t longer = (each + 1) * rest;
+    return (int)(tile < longer ? div_by(tile, each + 1) : rest + div_by(tile - longer, each));
+  }
+};
 __device__ __forceinline__ int used_ctas(int64_t total, int grid) {
-  const int64_t want = (total + AT_MIN_TILES - 1) / AT_MIN_TILES;
+  const int64_t want = div_by(total + AT_MIN_TILES - 1, AT_MIN_TILES);
   return want < grid ? (int)(want < 1 ? 1 : want) : grid;
 }
 
@@ -514,19 +554,35 @@ __device__ __forceinline__ RowAt row_at(const AttendArgs& a, int b, int kvh, int
   return {kvh * a.G + row - tok * a.G, b * a.n_q + tok};
 }
 
-template <int D, bool R8>
-__global__ void __launch_bounds__(AT_THREADS, AT_PER_SM) k_cache_attend(const __grid_constant__ AttendArgs a) {
-  pdl_prologue();
+// NQ: n8 tiles of query rows (1: up to 8 rows of a KV head and request, 2: 16 at a time)
+template <int D, int NQ>
+__global__ void __launch_bounds__(AT_THREADS, at_per_sm(D, NQ))
+k_cache_attend(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV, const __grid_constant__ AttendArgs a) {
   using L = AttendSmem<D>;
   constexpr int NST = L::NST;
   constexpr int CH = D / 16;      // 16-byte chunks of a row
-  constexpr int KS = D / 16;      // k-steps of Q K^T
-  constexpr int NT = D / 8;       // n-tiles of P V
-  constexpr int ROWS = R8 ? 8 : 16;
-  extern __shared__ __align__(16) uint8_t smem[];
+  constexpr int KS = D / 16;      // k-steps of K Q^T
+  constexpr int MTV = D / 16;     // m-tiles of V^T P^T
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   int* pre = reinterpret_cast<int*>(smem + L::PRE);
+  __shared__ int abort_word;
+  volatile int* abort_flag = &abort_word;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int g = lane >> 2, tq = lane & 3;
+  uint8_t* ring = smem + warp * NST * 2 * L::BOX;
+  float2* scales = reinterpret_cast<float2*>(smem + L::SC) + warp * NST;
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + L::BAR) + warp * NST;
+  if (tid == 0) abort_word = 0;
+  if (lane == 0) {
+    for (int i = 0; i < NST; ++i) mbar_init(&full[i], 1);
+    fence_barrier_init();
+    if (warp == 0) {
+      tma_prefetch_desc(&tmK);
+      tma_prefetch_desc(&tmV);
+    }
+  }
+  pdl_prologue();
   const int U = a.Hkv * a.MT;
   const int total_req = scan_tiles(a, pre, blockIdx.x == 0);
   const int64_t total = (int64_t)total_req * U;
@@ -544,17 +600,18 @@ __global__ void __launch_bounds__(AT_THREADS, AT_PER_SM) k_cache_attend(const __
   }
   const int ctas = used_ctas(total, gridDim.x);
   if (total == 0 || (int)blockIdx.x >= ctas) return;
-  const int64_t from = cut_at(total, ctas, blockIdx.x), to = cut_at(total, ctas, blockIdx.x + 1);
-
-  const uint32_t ring = smem_u32(smem) + warp * NST * L::STAGE;
-  const uint8_t* ring_p = smem + warp * NST * L::STAGE;
+  const Cut cut(total, ctas);
+  const int64_t from = cut.first(blockIdx.x), to = cut.first(blockIdx.x + 1);
+  uint32_t phases = 0;  // bit: parity that the stage's next load completes
+  uint32_t flying = 0;  // bit: the stage has a load that nobody has waited for
+  bool dead = false;    // a wait ran out: nothing is loaded or computed from here on
 
   for (int64_t at = from; at < to;) {
     // the unit (request, KV head, row tile) that holds tile `at`
-    const int b = owner_of(pre, a.n_req, (int)(at / U));
+    const int b = owner_of(pre, a.n_req, (int)div_by(at, U));
     const int tiles = pre[b + 1] - pre[b];
     const int64_t base = (int64_t)pre[b] * U;
-    const int unit = (int)((at - base) / tiles);
+    const int unit = (int)div_by(at - base, tiles);
     const int64_t unit0 = base + (int64_t)unit * tiles;
     const int t0 = (int)(at - unit0);
     const int t1 = (int)min((int64_t)tiles, to - unit0);
@@ -563,15 +620,70 @@ __global__ void __launch_bounds__(AT_THREADS, AT_PER_SM) k_cache_attend(const __
     const int rows = a.n_q * a.G;
     at = unit0 + t1;
 
-    // Q: this lane's rows g and g + 8, scaled by a power of two per row into fp16
-    uint32_t qa[KS][4];
-    float rowf[2];
-    int limit[2];  // last key that the row sees
+    const int steps = t1 - t0;
+    const int32_t* trow = a.table + (int64_t)b * a.width;
+    // page numbers and scales of 32 steps at a time, one per lane
+    auto load_page = [&](int i0) {
+      const int key = (t0 + i0 + lane) * AT_TILE + warp * AT_KEYS;
+      return i0 + lane < steps && key < len ? trow[key >> a.shift] : -1;
+    };
+    auto load_scales = [&](int i0, int& pg) {
+      float2 sc = make_float2(0.f, 0.f);
+      const int key = (t0 + i0 + lane) * AT_TILE + warp * AT_KEYS;
+      if (i0 + lane < steps && key < len) {
+        if (pg < 0 || pg >= a.num_pages) {
+          report(a.status, DSA_ERR_DEVICE, DETAIL_BAD_PAGE);
+          pg = -1;
+        } else {
+          sc = make_float2(a.k_scale[(int64_t)pg * a.Hkv + kvh], a.v_scale[(int64_t)pg * a.Hkv + kvh]);
+          if (!(good_scale(sc.x) && good_scale(sc.y))) {
+            report(a.status, DSA_ERR_DEVICE, DETAIL_BAD_SCALE);
+            sc = make_float2(0.f, 0.f);
+            pg = -1;
+          }
+        }
+      }
+      return sc;
+    };
+    int page = load_page(0), page_next = load_page(32);
+    float2 sc = load_scales(0, page), sc_next = make_float2(0.f, 0.f);
+    int win = 0;   // steps whose pages `page` begins with
+    int put = 0;   // stage of the next step to be loaded
+    auto issue = [&](int i) {
+      if (i < steps) {
+        const int at_lane = i - win;
+        const int pg = __shfl_sync(0xffffffffu, page, at_lane);
+        if (lane == at_lane) scales[put] = sc;
+        if (pg >= 0 && !dead) flying |= 1u << put;
+        if (pg >= 0 && !dead && lane == 0) {
+          uint8_t* dst = ring + put * 2 * L::BOX;
+          const int token = ((t0 + i) * AT_TILE + warp * AT_KEYS) & ((1 << a.shift) - 1);
+          mbar_arrive_expect_tx(&full[put], 2 * L::BOX);
+          tma_load_rows(dst, &tmK, &full[put], token, kvh, pg);
+          tma_load_rows(dst + L::BOX, &tmV, &full[put], token, kvh, pg);
+        }
+        if (at_lane == 15) sc_next = load_scales(win + 32, page_next);
+        if (at_lane == 31) {
+          win += 32;
+          page = page_next;
+          sc = sc_next;
+          page_next = load_page(win + 32);
+        }
+      }
+      put = put + 1 == NST ? 0 : put + 1;
+    };
+
+#pragma unroll 1
+    for (int i = 0; i < NST - 1; ++i) issue(i);
+
+    // Q: row 8 n + g of the tile, this lane's 16-byte chunks, scaled by a power of two per row into fp16
+    uint32_t qb[NQ][KS][2];
+    float rowf[NQ][2];  // what turns a product of row 8 n + 2 tq + x into log2 units (without the key's scale)
+    int limit[NQ][2];   // the last key that this row sees
 #pragma unroll
-    for (int x = 0; x < 2; ++x) {
-      const int row = mt * 16 + g + 8 * x;
-      const bool live = row < rows && !(R8 && x == 1);
-      limit[x] = live ? len - a.n_q + row / a.G : -1;
+    for (int n = 0; n < NQ; ++n) {
+      const int row = mt * 16 + 8 * n + g;
+      const bool live = row < rows;
       uint32_t w[CH / 4][8];
       const RowAt ra = row_at(a, b, kvh, live ? row : 0);
       const __nv_bfloat16* q = a.Q + ra.head * a.q_hs + (int64_t)ra.token * a.q_ts;
@@ -594,7 +706,6 @@ __global__ void __launch_bounds__(AT_THREADS, AT_PER_SM) k_cache_attend(const __
       const int e = (int)(mx >> 7);                        // biased exponent of the row's largest value
       const int up = e == 0 ? 0 : max(-114, min(110, 127 + 13 - e));  // brings it to [2^13, 2^14)
       const float f = pow2f(up);
-      rowf[x] = a.scale_log2 * pow2f(-up);
 #pragma unroll
       for (int i = 0; i < CH / 4; ++i) {
 #pragma unroll
@@ -602,171 +713,135 @@ __global__ void __launch_bounds__(AT_THREADS, AT_PER_SM) k_cache_attend(const __
 #pragma unroll
           for (int k = 0; k < 2; ++k) {
             const uint32_t p = w[i][2 * s + k];
-            qa[4 * i + s][2 * k + x] = f16x2(__uint_as_float(p << 16) * f, __uint_as_float(p & 0xffff0000u) * f);
+            qb[n][4 * i + s][k] = f16x2(__uint_as_float(p << 16) * f, __uint_as_float(p & 0xffff0000u) * f);
           }
         }
+      }
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        rowf[n][x] = __shfl_sync(0xffffffffu, a.scale_log2 * pow2f(-up), (2 * tq + x) * 4);
+        const int r = mt * 16 + 8 * n + 2 * tq + x;
+        limit[n][x] = r < rows ? len - a.n_q + r / a.G : -1;
       }
     }
     const int see_all = len - a.n_q;  // every row sees the keys up to here
 
-    float o[NT][4];
+    float o[NQ][MTV][4];
 #pragma unroll
-    for (int i = 0; i < NT; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
-    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
-
-    const int steps = t1 - t0;
-    const int32_t* trow = a.table + (int64_t)b * a.width;
-    // page numbers of 32 steps at a time, one per lane
-    auto load_pages = [&](int i0) {
-      const int key = (t0 + i0 + lane) * AT_TILE + warp * AT_KEYS;
-      int pg = -1;
-      if (i0 + lane < steps && key < len) {
-        pg = trow[key >> a.shift];
-        if (pg < 0 || pg >= a.num_pages) {
-          report(a.status, DSA_ERR_DEVICE, DETAIL_BAD_PAGE);
-          pg = -1;
-        }
-      }
-      return pg;
-    };
-    int pages = load_pages(0), pages_next = load_pages(32);
-    int seen = 0;  // steps whose pages `pages` begins with
-    uint32_t have = 0;  // bit: ring stage holds keys
-
-    auto issue = [&](int i) {
-      const uint32_t st = (uint32_t)i % NST;
-      have &= ~(1u << st);
-      if (i < steps) {
-        if (i - seen >= 32) {
-          seen += 32;
-          pages = pages_next;
-          pages_next = load_pages(seen + 32);
-        }
-        const int pg = __shfl_sync(0xffffffffu, pages, i - seen);
-        if (pg >= 0) {
-          have |= 1u << st;
-          const int key = (t0 + i) * AT_TILE + warp * AT_KEYS;
-          const int64_t off = pg * a.page_stride + kvh * a.head_stride + (key & ((1 << a.shift) - 1)) * a.token_stride;
-          const uint32_t dst = ring + st * L::STAGE;
+    for (int n = 0; n < NQ; ++n)
 #pragma unroll
-          for (int k = 0; k < AT_KEYS * CH / 32; ++k) {
-            const int r = (k * 32 + lane) / CH, c = (k * 32 + lane) % CH;
-            // chunk places that keep the reads below free of bank conflicts (rows of 128 bytes)
-            const int ck = D == 128 ? c ^ (((r & 1) << 2) | ((r >> 1) & 3)) : c;
-            const int cv = D == 128 ? c ^ (((r >> 1) & 3) << 1) : c ^ ((r >> 1) & 3);
-            cp_async16(dst + r * D + ck * 16, a.K + off + r * a.token_stride + c * 16);
-            cp_async16(dst + AT_KEYS * D + r * D + cv * 16, a.V + off + r * a.token_stride + c * 16);
-          }
-          if (lane < 2) {
-            const float* s = lane ? a.v_scale : a.k_scale;
-            cp_async4(dst + AT_KEYS * D * 2 + lane * 4, s + (int64_t)pg * a.Hkv + kvh);
-          }
-        }
-      }
-      cp_commit();
-    };
+      for (int i = 0; i < MTV; ++i) o[n][i][0] = o[n][i][1] = o[n][i][2] = o[n][i][3] = 0.f;
+    float m[NQ][2], l[NQ][2];
+#pragma unroll
+    for (int n = 0; n < NQ; ++n) {
+      m[n][0] = m[n][1] = -INFINITY;
+      l[n][0] = l[n][1] = 0.f;
+    }
 
-#pragma unroll 1
-    for (int i = 0; i < NST - 1; ++i) issue(i);
+    int got = 0;  // stage of step i
 #pragma unroll 1
     for (int i = 0; i < steps; ++i) {
-      cp_wait<NST - 2>();
       __syncwarp();
-      const uint32_t st = (uint32_t)i % NST;
-      const uint8_t* kp = ring_p + st * L::STAGE;
-      const uint8_t* vp = kp + AT_KEYS * D;
-      const float2 sc = *reinterpret_cast<const float2*>(kp + AT_KEYS * D * 2);
-      bool use = (have >> st) & 1u;
-      if (use && !(good_scale(sc.x) && good_scale(sc.y))) {
-        if (lane == 0) report(a.status, DSA_ERR_DEVICE, DETAIL_BAD_SCALE);
-        use = false;
+      const float2 ss = scales[got];
+      const uint8_t* kp = ring + got * 2 * L::BOX;
+      const uint8_t* vp = kp + L::BOX;
+      bool use = ss.x > 0.f && !dead;
+      if (use) {
+        if (!serve_warp_wait(&full[got], (phases >> got) & 1u, a.wait_limit_ns, a.status, DETAIL_WAIT_K, abort_flag, true)) {
+          dead = true;
+          use = false;
+        } else {
+          phases ^= 1u << got;
+          flying &= ~(1u << got);
+        }
       }
       if (use) {
         const int key0 = (t0 + i) * AT_TILE + warp * AT_KEYS;
-        // S = Q K^T: n-tile j holds keys key0 + 8 j + (0 .. 7)
-        float s[2][4];
+        // S^T = K Q^T: rows g and g + 8 of the m-tile are keys key0 + key_of(g) and 8 more
+        float s[NQ][4];
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          s[j][0] = s[j][1] = s[j][2] = s[j][3] = 0.f;
-          const int r = 8 * j + g;
+        for (int n = 0; n < NQ; ++n) s[n][0] = s[n][1] = s[n][2] = s[n][3] = 0.f;
+        const int r0 = key_of<D>(g);
 #pragma unroll
-          for (int i2 = 0; i2 < CH / 4; ++i2) {
-            const int c = tq + 4 * i2;
-            const int ck = D == 128 ? c ^ (((r & 1) << 2) | ((r >> 1) & 3)) : c;
-            const uint4 w = *reinterpret_cast<const uint4*>(kp + r * D + ck * 16);
-            const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
+        for (int i2 = 0; i2 < CH / 4; ++i2) {
+          const int c = tq + 4 * i2;
+          const int ck = D == 128 ? c ^ r0 : c ^ ((r0 >> 1) & 3);
+          const uint4 w0 = *reinterpret_cast<const uint4*>(kp + r0 * D + ck * 16);
+          const uint4 w1 = *reinterpret_cast<const uint4*>(kp + (r0 + 8) * D + ck * 16);
+          const uint32_t u0[4] = {w0.x, w0.y, w0.z, w0.w}, u1[4] = {w1.x, w1.y, w1.z, w1.w};
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
-              mma_f16(s[j], qa[4 * i2 + k], e4m3x2_to_f16x2(ww[k]), e4m3x2_to_f16x2(ww[k] >> 16));
+          for (int k = 0; k < 4; ++k) {
+            const uint32_t ka[4] = {e4m3x2_to_f16x2(u0[k]), e4m3x2_to_f16x2(u1[k]), e4m3x2_to_f16x2(u0[k] >> 16),
+                                    e4m3x2_to_f16x2(u1[k] >> 16)};
+#pragma unroll
+            for (int n = 0; n < NQ; ++n) mma_f16(s[n], ka, qb[n][4 * i2 + k][0], qb[n][4 * i2 + k][1]);
           }
         }
-        // V: rows 2 tq, 2 tq + 1, 2 tq + 8, 2 tq + 9 at this lane's D / 8 values
+        // V: the keys of k = 2 tq, 2 tq + 1, 2 tq + 8, 2 tq + 9, this lane's D / 8 values (from (D / 8) g on)
         uint32_t vw[4][D / 32];
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
-          const int r = 2 * tq + (u & 1) + 8 * (u >> 1);
+          const int r = key_of<D>(2 * tq + (u & 1)) + 8 * (u >> 1);
           if constexpr (D == 128) {
-            const uint4 w = *reinterpret_cast<const uint4*>(vp + r * D + ((g ^ (((r >> 1) & 3) << 1)) * 16));
+            const uint4 w = *reinterpret_cast<const uint4*>(vp + r * D + ((g ^ (r & 7)) * 16));
             vw[u][0] = w.x; vw[u][1] = w.y; vw[u][2] = w.z; vw[u][3] = w.w;
           } else {
             const uint2 w = *reinterpret_cast<const uint2*>(vp + r * D + (((g >> 1) ^ ((r >> 1) & 3)) * 16 + (g & 1) * 8));
             vw[u][0] = w.x; vw[u][1] = w.y;
           }
         }
-        const float lv = log2f(sc.y), iv = 1.f / sc.y;
-        float y[2][4];
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-#pragma unroll
-          for (int k = 0; k < 4; ++k) y[j][k] = fmaf(s[j][k], rowf[k >> 1] * sc.x, lv);
-        }
+        const float lv = log2f(ss.y), iv = 1.f / ss.y;
         const bool edge = key0 + AT_KEYS - 1 > see_all;  // some row does not see some key
-        if (edge) {
+        bool grow = false;
+        float y[NQ][4], top[NQ][2];
 #pragma unroll
-          for (int j = 0; j < 2; ++j) {
+        for (int n = 0; n < NQ; ++n) {
+#pragma unroll
+          for (int k = 0; k < 4; ++k) y[n][k] = fmaf(s[n][k], rowf[n][k & 1] * ss.x, lv);
+          if (edge) {
 #pragma unroll
             for (int k = 0; k < 4; ++k)
-              if (key0 + 8 * j + 2 * tq + (k & 1) > limit[k >> 1]) y[j][k] = -INFINITY;
+              if (key0 + r0 + 8 * (k >> 1) > limit[n][k & 1]) y[n][k] = -INFINITY;
+          }
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            top[n][x] = fmaxf(y[n][x], y[n][2 + x]);
+            grow |= top[n][x] > m[n][x] + P_LAG;
           }
         }
-        float top[2];
-#pragma unroll
-        for (int x = 0; x < 2; ++x) top[x] = fmaxf(fmaxf(y[0][2 * x], y[0][2 * x + 1]), fmaxf(y[1][2 * x], y[1][2 * x + 1]));
-        const bool grow = top[0] > m[0] + P_LAG || (!R8 && top[1] > m[1] + P_LAG);
         if (__any_sync(0xffffffffu, grow)) {
 #pragma unroll
-          for (int x = 0; x < (R8 ? 1 : 2); ++x) {
-            float t = fmaxf(m[x], top[x]);
-            t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 1));
-            t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 2));
-            if (t > m[x]) {
-              const float f = m[x] == -INFINITY ? 0.f : serve_ex2(m[x] - t);
-              m[x] = t;
-              l[x] *= f;
+          for (int n = 0; n < NQ; ++n) {
 #pragma unroll
-              for (int n = 0; n < NT; ++n) {
-                o[n][2 * x] *= f;
-                o[n][2 * x + 1] *= f;
+            for (int x = 0; x < 2; ++x) {
+              float t = fmaxf(m[n][x], top[n][x]);
+              t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 4));
+              t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 8));
+              t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 16));
+              const float f = t == m[n][x] ? 1.f : m[n][x] == -INFINITY ? 0.f : serve_ex2(m[n][x] - t);
+              m[n][x] = t;
+              l[n][x] *= f;
+#pragma unroll
+              for (int i2 = 0; i2 < MTV; ++i2) {
+                o[n][i2][x] *= f;
+                o[n][i2][2 + x] *= f;
               }
             }
           }
         }
-        uint32_t pa[4];
-        float sum[2] = {0.f, 0.f};
+        uint32_t pb[NQ][2];
 #pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          if (R8 && x == 1) {
-            pa[1] = pa[3] = 0u;
-            continue;
-          }
-          const float sh = m[x] == -INFINITY ? 0.f : P_OFF - m[x];
+        for (int n = 0; n < NQ; ++n) {
+          float p[4];
 #pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            const float p0 = serve_ex2(y[j][2 * x] + sh), p1 = serve_ex2(y[j][2 * x + 1] + sh);
-            sum[x] += p0 + p1;
-            pa[2 * j + x] = f16x2(p0, p1);
+          for (int x = 0; x < 2; ++x) {
+            const float sh = m[n][x] == -INFINITY ? 0.f : P_OFF - m[n][x];
+            p[x] = serve_ex2(y[n][x] + sh);
+            p[2 + x] = serve_ex2(y[n][2 + x] + sh);
+            l[n][x] = fmaf(p[x] + p[2 + x], iv, l[n][x]);
           }
-          l[x] = fmaf(sum[x], iv, l[x]);
+          pb[n][0] = transpose8x8(f16x2(p[0], p[1]));
+          pb[n][1] = transpose8x8(f16x2(p[2], p[3]));
         }
         if (edge) {
           // Values that a row must not see: those behind the length become 0; a NaN that only some
@@ -774,23 +849,23 @@ __global__ void __launch_bounds__(AT_THREADS, AT_PER_SM) k_cache_attend(const __
           uint32_t nan_any = 0;
 #pragma unroll
           for (int u = 0; u < 4; ++u) {
-            const bool behind = key0 + 2 * tq + (u & 1) + 8 * (u >> 1) >= len;
+            const bool behind = key0 + key_of<D>(2 * tq + (u & 1)) + 8 * (u >> 1) >= len;
 #pragma unroll
             for (int k = 0; k < D / 32; ++k) {
               if (behind) vw[u][k] = 0u;
-              const uint32_t w = vw[u][k];
-              nan_any |= ((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;  // a byte of 0x7f or 0xff
+              nan_any |= ((vw[u][k] & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;  // a byte of 0x7f or 0xff
             }
           }
           if (__any_sync(0xffffffffu, nan_any != 0u)) {
-            uint32_t one[4];  // 1 where the row sees the key
+            uint32_t one[NQ][2];  // 1 where row 8 n + g sees the key
 #pragma unroll
-            for (int x = 0; x < 2; ++x) {
+            for (int n = 0; n < NQ; ++n) {
+              const int r = mt * 16 + 8 * n + g;
+              const int lim = r < rows ? len - a.n_q + r / a.G : -1;
 #pragma unroll
-              for (int j = 0; j < 2; ++j) {
-                const int key = key0 + 8 * j + 2 * tq;
-                one[2 * j + x] = (key <= limit[x] ? 0x3c00u : 0u) | (key + 1 <= limit[x] ? 0x3c000000u : 0u);
-              }
+              for (int j = 0; j < 2; ++j)
+                one[n][j] = (key0 + key_of<D>(2 * tq) + 8 * j <= lim ? 0x3c00u : 0u) |
+                            (key0 + key_of<D>(2 * tq + 1) + 8 * j <= lim ? 0x3c000000u : 0u);
             }
 #pragma unroll
             for (int k = 0; k < D / 32; ++k) {
@@ -802,56 +877,75 @@ __global__ void __launch_bounds__(AT_THREADS, AT_PER_SM) k_cache_attend(const __
                 vw[u][k] &= ~(hit * 0xffu);
               }
 #pragma unroll
-              for (int z = 0; z < 4; ++z) {
-                const uint32_t sel = z | ((4 + z) << 4);
-                float c[4] = {0.f, 0.f, 0.f, 0.f};
-                mma_f16(c, one, e4m3x2_to_f16x2(prmt(nb[0], nb[1], sel)), e4m3x2_to_f16x2(prmt(nb[2], nb[3], sel)));
+              for (int z = 0; z < 2; ++z) {
+                const uint32_t p01 = prmt(nb[0], nb[1], z ? 0x7362 : 0x5140), p89 = prmt(nb[2], nb[3], z ? 0x7362 : 0x5140);
+                const uint32_t na[4] = {e4m3x2_to_f16x2(p01), e4m3x2_to_f16x2(p01 >> 16), e4m3x2_to_f16x2(p89), e4m3x2_to_f16x2(p89 >> 16)};
 #pragma unroll
-                for (int q = 0; q < 4; ++q)
-                  if (c[q] > 0.f) o[4 * k + z][q] = __int_as_float(0x7fffffff);
+                for (int n = 0; n < NQ; ++n) {
+                  float c[4] = {0.f, 0.f, 0.f, 0.f};
+                  mma_f16(c, na, one[n][0], one[n][1]);
+#pragma unroll
+                  for (int q = 0; q < 4; ++q)
+                    if (c[q] > 0.f) o[n][2 * k + z][q] = __int_as_float(0x7fffffff);
+                }
               }
             }
           }
         }
-        // O += P V: n-tile e holds value e of every lane's stretch
+        // O^T += V^T P^T: rows g and g + 8 of m-tile t are values 2 t and 2 t + 1 of every lane's stretch
 #pragma unroll
         for (int k = 0; k < D / 32; ++k) {
-          const uint32_t a01 = prmt(vw[0][k], vw[1][k], 0x5140), a23 = prmt(vw[0][k], vw[1][k], 0x7362);
-          const uint32_t b01 = prmt(vw[2][k], vw[3][k], 0x5140), b23 = prmt(vw[2][k], vw[3][k], 0x7362);
-          mma_f16(o[4 * k], pa, e4m3x2_to_f16x2(a01), e4m3x2_to_f16x2(b01));
-          mma_f16(o[4 * k + 1], pa, e4m3x2_to_f16x2(a01 >> 16), e4m3x2_to_f16x2(b01 >> 16));
-          mma_f16(o[4 * k + 2], pa, e4m3x2_to_f16x2(a23), e4m3x2_to_f16x2(b23));
-          mma_f16(o[4 * k + 3], pa, e4m3x2_to_f16x2(a23 >> 16), e4m3x2_to_f16x2(b23 >> 16));
+#pragma unroll
+          for (int z = 0; z < 2; ++z) {
+            const uint32_t p01 = prmt(vw[0][k], vw[1][k], z ? 0x7362 : 0x5140), p89 = prmt(vw[2][k], vw[3][k], z ? 0x7362 : 0x5140);
+            const uint32_t va[4] = {e4m3x2_to_f16x2(p01), e4m3x2_to_f16x2(p01 >> 16), e4m3x2_to_f16x2(p89), e4m3x2_to_f16x2(p89 >> 16)};
+#pragma unroll
+            for (int n = 0; n < NQ; ++n) mma_f16(o[n][2 * k + z], va, pb[n][0], pb[n][1]);
+          }
         }
       }
-      __syncwarp();
+      __syncwarp();  // the stage before this one has been read by every lane
       issue(i + NST - 1);
+      got = got + 1 == NST ? 0 : got + 1;
     }
-    cp_wait<0>();
 
     // join the warps: O rows, m and l through shared memory
 #pragma unroll
-    for (int x = 0; x < 2; ++x) {
-      l[x] += __shfl_xor_sync(0xffffffffu, l[x], 1);
-      l[x] += __shfl_xor_sync(0xffffffffu, l[x], 2);
+    for (int n = 0; n < NQ; ++n) {
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        l[n][x] += __shfl_xor_sync(0xffffffffu, l[n][x], 4);
+        l[n][x] += __shfl_xor_sync(0xffffffffu, l[n][x], 8);
+        l[n][x] += __shfl_xor_sync(0xffffffffu, l[n][x], 16);
+      }
+    }
+    if (dead) {  // loads under way end before the ring is used for something else
+      if (lane == 0)
+        for (int i = 0; i < NST; ++i)
+          if ((flying >> i) & 1u) serve_drain(&full[i], (phases >> i) & 1u);
+      flying = 0;
+      __syncwarp();
     }
     __syncthreads();  // every warp is done with its ring
     float* join = reinterpret_cast<float*>(smem);  // [warp][16][D + 4]: m, l, then O at 4
 #pragma unroll
-    for (int x = 0; x < (R8 ? 1 : 2); ++x) {
-      float* w = join + (warp * 16 + g + 8 * x) * (D + 4);
-      if (tq == 0) {
-        w[0] = m[x];
-        w[1] = l[x];
-      }
+    for (int n = 0; n < NQ; ++n) {
 #pragma unroll
-      for (int n = 0; n < NT; ++n) {
-        w[4 + (D / 8) * (2 * tq) + n] = o[n][2 * x];
-        w[4 + (D / 8) * (2 * tq + 1) + n] = o[n][2 * x + 1];
+      for (int x = 0; x < 2; ++x) {
+        float* w = join + (warp * 16 + 8 * n + 2 * tq + x) * (D + 4);
+        if (g == 0) {
+          w[0] = m[n][x];
+          w[1] = l[n][x];
+        }
+#pragma unroll
+        for (int i = 0; i < MTV; ++i) {
+          w[4 + (D / 8) * g + 2 * i] = o[n][i][x];
+          w[4 + (D / 8) * g + 2 * i + 1] = o[n][i][2 + x];
+        }
       }
     }
     __syncthreads();
-    const int in_tile = min(ROWS, rows - mt * 16);
+    const int in_tile = min(8 * NQ, rows - mt * 16);
     const bool whole = t0 == 0 && t1 == tiles;
     constexpr int TPR = D / 8;  // threads of a row
     for (int i = tid; i < in_tile * TPR; i += AT_THREADS) {
@@ -891,50 +985,67 @@ __global__ void __launch_bounds__(AT_THREADS, AT_PER_SM) k_cache_attend(const __
         *reinterpret_cast<float4*>(w + 8 + c) = make_float4(acc[4], acc[5], acc[6], acc[7]);
       }
     }
+    fence_proxy_async_smem();
     __syncthreads();  // the ring may be filled again
   }
 }
 
 // Units that a range's end cut: adds their parts in range order.  A part of the unit's first tiles
 // is its CTA's last one (slot 1), every other part is its CTA's first (slot 0).
+// One lane per part for the maxima and sums, then one lane per 4 columns for O.
 template <int D>
 __global__ void __launch_bounds__(AT_THREADS) k_cache_join(const __grid_constant__ AttendArgs a, int grid) {
   extern __shared__ int pre[];
   // the lengths were written before the kernel in front of this one began, so they can be read before it ends
   const int U = a.Hkv * a.MT;
   const int64_t total = (int64_t)scan_tiles(a, pre, false) * U;
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int b = blockIdx.x / U, unit = blockIdx.x - b * U;
   const int tiles = pre[b + 1] - pre[b];
-  if (tiles == 0) return;
-  const int ctas = used_ctas(total, grid);
-  const int64_t u0 = (int64_t)pre[b] * U + (int64_t)unit * tiles, u1 = u0 + tiles;
-  // the CTAs whose ranges hold the unit's first and last tile: cut_at(c) <= tile < cut_at(c + 1)
-  const int c0 = (int)(((u0 + 1) * ctas - 1) / total), c1 = (int)((u1 * ctas - 1) / total);
-  if (c0 == c1) return;
+  const int64_t u0 = (int64_t)pre[b] * U + (int64_t)unit * tiles;
+  const Cut cut(max(total, (int64_t)1), used_ctas(total, grid));
+  const int c0 = cut.holder(u0), c1 = cut.holder(u0 + max(tiles, 1) - 1);  // the CTAs with the unit's first and last tile
   const int kvh = unit / a.MT, mt = unit - kvh * a.MT;
   const int rows = min(16, a.n_q * a.G - mt * 16);
-  constexpr int TPR = D / 4;
-  for (int i = threadIdx.x + blockIdx.y * AT_THREADS; i < rows * TPR; i += AT_THREADS * gridDim.y) {
-    const int row = i / TPR, c = (i % TPR) * 4;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  if (tiles == 0 || c0 == c1) return;
+  constexpr int TPR = D / 4;  // lanes of a row: 32 or 16
+  const int lane = threadIdx.x & 31, sub = lane % TPR, c = sub * 4;
+  // (whole warps: the rows are padded to a multiple of what a warp takes)
+  const int per_warp = 32 / TPR;
+  for (int r0 = (blockIdx.y * AT_WARPS + (threadIdx.x >> 5)) * per_warp; r0 < rows; r0 += AT_WARPS * per_warp * gridDim.y) {
+    const int row = r0 + lane / TPR;
+    const bool in = row < rows;
+    auto part = [&](int k) {  // the unit's first part is its CTA's last one, every other its CTA's first
+      return a.part + ((int64_t)((c0 + k) * 2 + (k == 0 ? 1 : 0)) * 16 + (in ? row : 0)) * (D + 4);
+    };
+    const int n = c1 - c0 + 1;
     float M = -INFINITY;
-    for (int k = c0; k <= c1; ++k) {
-      const int slot = cut_at(total, ctas, k) <= u0 ? 1 : 0;
-      M = fmaxf(M, a.part[((int64_t)(k * 2 + slot) * 16 + row) * (D + 4)]);
-    }
+    for (int k = sub; k < n; k += TPR) M = fmaxf(M, part(k)[0]);
+#pragma unroll
+    for (int o = TPR / 2; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
     float acc[4] = {0.f, 0.f, 0.f, 0.f}, lsum = 0.f;
-    for (int k = c0; k <= c1; ++k) {
-      const int slot = cut_at(total, ctas, k) <= u0 ? 1 : 0;
-      const float* w = a.part + ((int64_t)(k * 2 + slot) * 16 + row) * (D + 4);
-      const float f = w[0] == -INFINITY ? 0.f : serve_ex2(w[0] - M);
-      const float4 v = *reinterpret_cast<const float4*>(w + 4 + c);
-      lsum += w[1] * f;
-      acc[0] += v.x * f;
-      acc[1] += v.y * f;
-      acc[2] += v.z * f;
-      acc[3] += v.w * f;
+    for (int k0 = 0; k0 < n; k0 += TPR) {
+      float f = 0.f;
+      if (k0 + sub < n) {
+        const float* w = part(k0 + sub);
+        f = w[0] == -INFINITY ? 0.f : serve_ex2(w[0] - M);
+        lsum += w[1] * f;
+      }
+      const int m = min(TPR, n - k0);
+#pragma unroll 8
+      for (int k = 0; k < m; ++k) {
+        const float4 v = *reinterpret_cast<const float4*>(part(k0 + k) + 4 + c);
+        const float fk = __shfl_sync(0xffffffffu, f, k, TPR);
+        acc[0] += v.x * fk;
+        acc[1] += v.y * fk;
+        acc[2] += v.z * fk;
+        acc[3] += v.w * fk;
+      }
     }
+#pragma unroll
+    for (int o = TPR / 2; o > 0; o >>= 1) lsum += __shfl_xor_sync(0xffffffffu, lsum, o);
+    if (!in) continue;
     const RowAt ra = row_at(a, b, kvh, mt * 16 + row);
     const float inv = lsum == 0.f ? 0.f : 1.f / lsum;
     const __nv_bfloat162 v0 = __floats2bfloat162_rn(acc[0] * inv, acc[1] * inv), v1 = __floats2bfloat162_rn(acc[2] * inv, acc[3] * inv);
@@ -964,16 +1075,43 @@ dsa_status validate_cache(const dsa_cache* c) {
   return DSA_OK;
 }
 
-template <int D, bool R8>
-dsa_status launch_attend(AttendArgs& a, cudaStream_t stream) {
+using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
+                                 const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                 CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+// Tensor map over K or V of a cache: [page][head][token][byte], boxes of 16 rows.
+bool make_cache_map(CUtensorMap* map, void* base, const dsa_cache& c) {
+  static const EncodeTiled encode = [] {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q) != cudaSuccess || q != cudaDriverEntryPointSuccess)
+      p = nullptr;
+    return reinterpret_cast<EncodeTiled>(p);
+  }();
+  if (encode == nullptr) return false;
+  const cuuint64_t dims[4] = {(cuuint64_t)c.d, (cuuint64_t)c.page, (cuuint64_t)c.Hkv, (cuuint64_t)c.num_pages};
+  // strides of dimensions of size 1 are never used, but have to be valid
+  const int64_t head = c.Hkv > 1 ? c.head_stride : c.page * c.token_stride;
+  const int64_t page = c.num_pages > 1 ? c.page_stride : c.Hkv * head;
+  const cuuint64_t strides[3] = {(cuuint64_t)c.token_stride, (cuuint64_t)head, (cuuint64_t)page};
+  const cuuint32_t box[4] = {(cuuint32_t)c.d, (cuuint32_t)AT_KEYS, 1, 1}, one[4] = {1, 1, 1, 1};
+  return encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, base, dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                c.d == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int D, int NQ>
+dsa_status launch_attend(const dsa_cache& c, AttendArgs& a, cudaStream_t stream) {
+  CUtensorMap mk, mv;
+  if (!make_cache_map(&mk, c.K, c) || !make_cache_map(&mv, c.V, c)) return DSA_ERR_CUDA;
   int dev = 0, sms = 0;
   cudaError_t e = serve_sms(&dev, &sms);
-  if (e == cudaSuccess) e = serve_allow_smem<k_cache_attend<D, R8>>(dev, AttendSmem<D>::bytes(MAX_REQ));
+  if (e == cudaSuccess) e = serve_allow_smem<k_cache_attend<D, NQ>>(dev, AttendSmem<D>::bytes(MAX_REQ));
   const int smem = AttendSmem<D>::bytes(a.n_req);
-  const int grid = min(AT_PER_SM * sms, AT_MAX_CTAS);
-  if (e == cudaSuccess) e = launch_pdl(k_cache_attend<D, R8>, dim3(grid), dim3(AT_THREADS), (size_t)smem, stream, a);
+  const int grid = min(at_per_sm(D, NQ) * sms, AT_MAX_CTAS);
+  if (e == cudaSuccess) e = launch_pdl(k_cache_attend<D, NQ>, dim3(grid), dim3(AT_THREADS), (size_t)smem, stream, mk, mv, a);
   const int rows = min(16, a.n_q * a.G);
-  const int per_unit = max(1, rows * (D / 4) / AT_THREADS);
+  const int per_unit = ceil_div(rows * (D / 4), AT_THREADS);
   if (e == cudaSuccess)
     e = launch_pdl(k_cache_join<D>, dim3(a.n_req * a.Hkv * a.MT, per_unit), dim3(AT_THREADS), (size_t)(a.n_req + 1) * 4, stream, a, grid);
   if (e == cudaSuccess) e = cudaGetLastError();
@@ -1129,9 +1267,10 @@ dsa_status dsa_cache_attention(const dsa_cache* cache, const void* Q, int32_t Hq
   a.T = n_req * n_q;
   a.scale_log2 = (float)(1.4426950408889634 / sqrt((double)cache->d));
   a.status = st;
-  const bool r8 = n_q * a.G <= 8;
-  if (cache->d == 128) return r8 ? launch_attend<128, true>(a, (cudaStream_t)stream) : launch_attend<128, false>(a, (cudaStream_t)stream);
-  return r8 ? launch_attend<64, true>(a, (cudaStream_t)stream) : launch_attend<64, false>(a, (cudaStream_t)stream);
+  a.wait_limit_ns = wait_limit_ns();
+  const bool one = n_q * a.G <= 8;
+  if (cache->d == 128) return one ? launch_attend<128, 1>(*cache, a, (cudaStream_t)stream) : launch_attend<128, 2>(*cache, a, (cudaStream_t)stream);
+  return one ? launch_attend<64, 1>(*cache, a, (cudaStream_t)stream) : launch_attend<64, 2>(*cache, a, (cudaStream_t)stream);
 }
 
 }  // extern "C"

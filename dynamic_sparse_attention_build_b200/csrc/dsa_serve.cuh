@@ -90,7 +90,7 @@ static __device__ __noinline__ bool serve_wait_loop(uint64_t* bar, uint32_t pari
   uint32_t spins = 0;
   while (true) {
     if (poll ? mbar_test_wait(bar, parity) : mbar_try_wait(bar, parity)) return true;
-    if (((++spins) & 31u) == 0u) {
+    if (((++spins) & 7u) == 0u) {
       if (*abort_flag) return false;
       if (globaltimer_ns() - t0 > limit) {
         report_timeout(status, detail, abort_flag);

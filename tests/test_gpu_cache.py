@@ -409,6 +409,28 @@ def test_attention_gives_the_same_bits_each_time(dsa):
         assert torch.equal(O, want) and torch.equal(lse, want_lse)
 
 
+def test_waits_that_run_out_leave_the_next_launch_exact(dsa):
+    from dynamic_sparse_attention_build_b200 import _binding as B
+    lens = [60000, 17, 50000, 70000]  # enough to fill the memory's bandwidth: loads take a few us
+    cache, table, dl, Q = attend_inputs(dsa, 8, 8, 128, 64, lens, 1)
+    want, want_lse = dsa.cache_attention(Q, cache, table, dl, want_lse=True)
+    assert dsa.device_status() == (0, 0)
+    out = 0
+    try:
+        for limit in (100, 300, 1000, 3000):
+            assert B.dsa_set_wait_limit(limit) == B.DSA_OK
+            dsa.cache_attention(Q, cache, table, dl)
+            status, _ = dsa.device_status()
+            assert status in (B.DSA_OK, B.DSA_ERR_TIMEOUT)
+            out += status == B.DSA_ERR_TIMEOUT
+    finally:
+        assert B.dsa_set_wait_limit(0) == B.DSA_OK
+    assert out > 0
+    O, lse = dsa.cache_attention(Q, cache, table, dl, want_lse=True)
+    assert dsa.device_status() == (0, 0)
+    assert torch.equal(O, want) and torch.equal(lse, want_lse)
+
+
 # --------------------------------------------------------------------------- together
 def test_serving_steps_together(dsa):
     """Prompts arrive, are prefilled and stored; decode steps follow, captured in one graph; one
