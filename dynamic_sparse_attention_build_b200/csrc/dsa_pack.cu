@@ -184,8 +184,12 @@ packed_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
       // ---------------------------------------------------------- items and TMA loads
       const bool by_heads = (a.G & 1) == 0;
       const int rows_per_item = by_heads ? TM : 2 * TM;
-      int win = 0, before = 0;       // sequence window (32 sequences), items groups before it
-      int lo = 0, hi = 0, incl = 0;  // this lane's sequence and the groups up to and with it
+      // Row groups are taken in windows of 32 sequences, one per lane, and in each window by their place in the
+      // sequence, the last (longest) ones first.
+      int win = 0, before = 0;         // first sequence of the window, groups of the windows before it
+      int lo = 0, hi = 0, groups = 0;  // this lane's sequence
+      int in_win = 0;                  // groups of the window
+      int place = 0, longer = 0;       // the place that items are taken from now, groups behind it
       auto load_window = [&]() {
         const int s = win + lane;
         lo = hi = 0;
@@ -197,12 +201,13 @@ packed_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
             hi = lo = 0;
           }
         }
-        incl = ceil_div(hi - lo, rows_per_item);
+        groups = ceil_div(hi - lo, rows_per_item);
+        in_win = warp_sum_int(groups);
+        int most = groups;
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-          const int v = __shfl_up_sync(0xffffffffu, incl, o);
-          if (lane >= o) incl += v;
-        }
+        for (int o = 16; o > 0; o >>= 1) most = max(most, __shfl_xor_sync(0xffffffffu, most, o));
+        place = most - 1;
+        longer = 0;
       };
       load_window();
       uint32_t gs = 0;   // ring stages used so far
@@ -213,14 +218,12 @@ packed_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
         const int64_t k = (int64_t)it * gridDim.x + ((it & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
         const int64_t grp64 = k / a.npairs;
         const int pair = (int)(k - grp64 * a.npairs);
-        int total = __shfl_sync(0xffffffffu, incl, 31);
-        while (grp64 >= (int64_t)before + total && win + 32 < a.nseq) {
-          before += total;
+        while (grp64 >= (int64_t)before + in_win && win + 32 < a.nseq) {
+          before += in_win;
           win += 32;
           load_window();
-          total = __shfl_sync(0xffffffffu, incl, 31);
         }
-        const bool end = grp64 >= (int64_t)before + total;
+        const bool end = grp64 >= (int64_t)before + in_win;
         const int slot = it % NITEM;
         PackItem* item = &items[slot];
         if (it >= NITEM) {
@@ -236,10 +239,17 @@ packed_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
           break;
         }
         const int grp = (int)(grp64 - before);
-        const int src = __popc(__ballot_sync(0xffffffffu, incl <= grp));  // first sequence whose groups reach past grp
+        uint32_t has = __ballot_sync(0xffffffffu, groups > place);  // sequences with a group at `place`
+        while (grp >= longer + __popc(has)) {
+          longer += __popc(has);
+          --place;
+          has = __ballot_sync(0xffffffffu, groups > place);
+        }
+        const bool mine = ((has >> lane) & 1u) && __popc(has & ((1u << lane) - 1u)) == grp - longer;
+        const int src = __ffs(__ballot_sync(0xffffffffu, mine)) - 1;
         const int start = __shfl_sync(0xffffffffu, lo, src);
         const int len = __shfl_sync(0xffffffffu, hi, src) - start;
-        const int local = __shfl_sync(0xffffffffu, incl, src) - 1 - grp;  // longest rows first
+        const int local = place;
         if (lane == 0) {
           PackItem& w = *item;
           w.start = start;
