@@ -299,3 +299,59 @@ def cache_attention(Q, cache, block_table, lens, n_q=1, O=None, lse=None, want_l
                 O.data_ptr(), *_strides(O), lse.data_ptr() if lse is not None else None, workspace.data_ptr(),
                 workspace.nbytes, st), "dsa_cache_attention")
     return O, lse
+
+
+class PagedLayer:
+    """One attention layer as a server keeps it for ``requests`` requests at a time: their page
+    tables, lengths and free pages, and the 8-bit cache of ``pages`` pages of ``page`` tokens.
+    A request may hold ``width`` pages at most.  ``prefill`` takes prompts, short ones packed or
+    one long one with sparse patterns, ``decode`` the tokens that follow.  Both enqueue work on
+    the current stream only, update lengths, tables and cache in place, and can be captured into
+    a CUDA graph.  Use it on one stream at a time.  If pages run out, no token of that call is
+    stored and ``status`` says DSA_ERR_CAPACITY."""
+
+    def __init__(self, Hq, Hkv, d, requests, pages, page=64, width=None, device="cuda"):
+        self.cache = PageCache.empty(pages, Hkv, page, d, device)
+        dev = self.cache.K.device
+        ints = dict(dtype=torch.int32, device=dev)
+        self.Hq, self.page, self.requests = Hq, page, requests
+        self.lens = torch.zeros(requests, **ints)
+        self.table = torch.full((requests, width or pages), -1, **ints)
+        self.free_pages = torch.arange(pages, **ints)
+        self.free_count = torch.full((1,), pages, **ints)
+        self.ones = torch.ones(requests, **ints)
+
+    def _store(self, K, V, new_lens):
+        T, n = K.shape[1], self.requests
+        new = torch.empty(T + n + 1, dtype=torch.int32, device=self.lens.device)
+        out = Tables(new[:T], new[T:], self.lens, self.free_count)
+        build_tables(self.lens, new_lens, self.free_pages, self.free_count, self.table, self.page, T, out=out)
+        cache_write(K, V, out.slots, self.cache)
+        return out
+
+    def prefill(self, Q, K, V, new_lens, patterns=None, block=64):
+        """Prompts of requests that hold no tokens yet.  Q [Hq, T, d], K and V [Hkv, T, d] hold
+        their rows one after the other (T may be larger than their sum: the rows behind the last
+        are undefined in O), new_lens (int32 [requests]) says how many each gets: 0 for a request
+        that gets none, -1 for one that has ended and gives its pages back.  With ``patterns``
+        (as for ``build_indices``) all T rows are one request's prompt.  Returns O."""
+        out = self._store(K, V, new_lens)
+        if patterns is None:
+            return packed_prefill(Q, K, V, out.cu_seqlens)[0]
+        from .api import build_indices, sparse_prefill
+        return sparse_prefill(Q, K, V, build_indices(Q, K, patterns, block))[0]
+
+    def decode(self, Q, K, V, new_lens=None, want_lse=False):
+        """The next tokens: Q [Hq, requests * n_q, d] holds n_q rows for each request, K and V
+        the rows of the requests that get tokens, one after the other.  new_lens defaults to one
+        token for every request; a request that gets fewer than n_q attends with its newest n_q
+        all the same.  Returns (O, lse or None)."""
+        if Q.shape[1] % self.requests:
+            _refuse(f"Q has {Q.shape[1]} rows for {self.requests} requests")
+        self._store(K, V, self.ones if new_lens is None else new_lens)
+        return cache_attention(Q, self.cache, self.table, self.lens, n_q=Q.shape[1] // self.requests, want_lse=want_lse)
+
+    def status(self):
+        """(status, detail) of the work on the current stream; synchronises it and clears the word."""
+        from .api import device_status
+        return device_status()

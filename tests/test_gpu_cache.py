@@ -496,6 +496,51 @@ def test_serving_steps_together(dsa):
     assert dsa.device_status() == (0, 0)
 
 
+def test_paged_layer(dsa):
+    """Short prompts packed, one long prompt with sparse patterns, decode steps of one and of two
+    tokens, a request that ends, and a prompt for which no pages are left."""
+    from dynamic_sparse_attention_build_b200 import _binding as B
+    Hq, Hkv, d, n = 4, 2, 64, 3
+    layer = dsa.PagedLayer(Hq, Hkv, d, n, pages=60, page=16, width=40)
+    g = gen(21)
+    new = lambda h, t: torch.randn(h, t, d, generator=g, device="cuda").bfloat16()  # noqa: E731
+    host = [0] * n
+
+    def check(O, lse, Q, n_q):
+        assert layer.lens.tolist() == host and layer.status() == (0, 0)
+        check_attend(O, lse, Q, layer.cache, layer.table, host, n_q)
+
+    Q, K, V = new(Hq, 50), new(Hkv, 50), new(Hkv, 50)
+    O = layer.prefill(Q, K, V, ints([20, 0, 27]))
+    host = [20, 0, 27]
+    for a, b in ((0, 20), (20, 47)):
+        for h in range(Hq):
+            plain.check_rows(O[h, a:b], None, Q[h, a:b], K[h // 2, a:b], V[h // 2, a:b], torch.arange(b - a, device="cuda"),
+                             plain.BF16, what="packed")
+    Q, K, V = new(Hq, 400), new(Hkv, 400), new(Hkv, 400)
+    pats = [dict(kind="ashape", sink=16, window=64)] * Hq
+    O = layer.prefill(Q, K, V, ints([0, 400, 0]), patterns=pats)
+    host[1] = 400
+    want, _ = dsa.sparse_prefill(Q, K, V, dsa.build_indices(Q, K, pats, 64))
+    assert torch.equal(O, want)
+    for _ in range(3):
+        Q = new(Hq, n)
+        O, lse = layer.decode(Q, new(Hkv, n), new(Hkv, n), want_lse=True)
+        host = [x + 1 for x in host]
+        check(O, lse, Q, 1)
+    Q = new(Hq, 2 * n)
+    O, lse = layer.decode(Q, new(Hkv, 4), new(Hkv, 4), ints([2, -1, 2]), want_lse=True)  # drafted tokens; request 1 ends
+    host = [host[0] + 2, 0, host[2] + 2]
+    check(O, lse, Q, 2)
+    assert host == [25, 0, 32] and layer.free_count.item() == 60 - 2 - 2
+    free = layer.free_pages.clone(), layer.table.clone()
+    layer.prefill(new(Hq, 1000), new(Hkv, 1000), new(Hkv, 1000), ints([0, 1000, 0]))
+    assert layer.status()[0] == B.DSA_ERR_CAPACITY
+    assert layer.lens.tolist() == host and torch.equal(free[0], layer.free_pages) and torch.equal(free[1], layer.table)
+    with pytest.raises(ValueError, match="rows"):
+        layer.decode(new(Hq, 4), new(Hkv, 3), new(Hkv, 3))
+
+
 @pytest.mark.parametrize("change, match", [
     (dict(Q="float"), "bfloat16"), (dict(Q="d"), "must be 64"), (dict(Q="rows"), "rows"), (dict(Q="heads"), "divide"),
     (dict(table="long"), "int32"), (dict(table="flat"), "block_table"), (dict(table="wide"), "contiguous"),
