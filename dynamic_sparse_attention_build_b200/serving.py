@@ -22,34 +22,19 @@ def _refuse(what):
     raise ValueError(what)
 
 
-class _on:
-    """The tensors' device and the call's stream made current: launches and allocations follow
-    them.  Entering gives the stream's handle."""
-    __slots__ = ("device", "stream", "held")
-
-    def __init__(self, device, stream):
-        self.device, self.stream, self.held = device, stream, None
-
-    def __enter__(self):
-        if self.stream is None and torch.cuda.current_device() == self.device.index:
-            return _raw_stream(self.device.index)
-        self.held = contextlib.ExitStack()
-        self.held.enter_context(torch.cuda.device(self.device))
-        if self.stream is None:
-            return _raw_stream(self.device.index)
-        if self.stream.device != self.device:
-            self.held.close()
-            raise ValueError(f"the stream belongs to {self.stream.device}, the tensors to {self.device}")
-        self.held.enter_context(torch.cuda.stream(self.stream))
-        return self.stream.cuda_stream
-
-    def __exit__(self, *why):
-        if self.held is not None:
-            self.held.close()
-
-
-# The handle of a device's current stream: 0.07 us, where torch.cuda.current_stream takes 3 us.
+# The handle of a device's current stream, and the current device: 0.1 us each, where
+# torch.cuda.current_stream takes 3 us.
 _raw_stream = torch._C._cuda_getCurrentRawStream
+_current_device = torch._C._cuda_getDevice
+
+
+@contextlib.contextmanager
+def _elsewhere(device, stream):
+    """The tensors' device and the call's stream made current: launches and allocations follow them."""
+    if stream is not None and stream.device != device:
+        _refuse(f"the stream belongs to {stream.device}, the tensors to {device}")
+    with torch.cuda.device(device), torch.cuda.stream(stream):  # (a stream of None changes nothing)
+        yield
 
 
 # Every message is put together only when it is needed: a call's checks take a few us otherwise.
@@ -63,11 +48,12 @@ def _tokens(name, t, heads=None, tokens=None, d=None, device=None):
     if device is not None and t.device != device:
         _refuse(f"{name} is on {t.device}, the call on {device}")
     shape = t.shape
-    for at, want in enumerate((heads, tokens, d)):
-        if want is not None and shape[at] != want:
-            _refuse(f"{name} has shape {tuple(shape)}; dimension {at} must be {want}")
-    if shape[2] != 64 and shape[2] != 128:
-        _refuse(f"{name}: d must be 64 or 128, not {shape[2]}")
+    h, n, e = shape
+    if (heads is not None and h != heads) or (tokens is not None and n != tokens) or (d is not None and e != d):
+        at = 0 if heads is not None and h != heads else 1 if tokens is not None and n != tokens else 2
+        _refuse(f"{name} has shape {tuple(shape)}; dimension {at} must be {(heads, tokens, d)[at]}")
+    if e != 64 and e != 128:
+        _refuse(f"{name}: d must be 64 or 128, not {e}")
     if t.stride(2) != 1:
         _refuse(f"{name}: the last dimension must be contiguous")
 
@@ -125,15 +111,18 @@ def packed_prefill(Q, K, V, cu_seqlens, O=None, lse=None, want_lse=False, stream
     _ints("cu_seqlens", cu_seqlens, cu_seqlens.shape, dev)
     if O is not None:
         _tokens("O", O, Hq, T, d, dev)
-    with _on(dev, stream) as st:
-        if O is None:
-            O = torch.empty_like(Q, memory_format=torch.contiguous_format)
-        lse = _lse(lse, want_lse, (Hq, T), dev)
-        if T > 0 and Hq > 0:
-            p = B.dsa_problem(Hq, Hkv, T, d, 64, 0, *_strides(Q), *_strides(K), *_strides(V), *_strides(O))
-            B.check(B.dsa_packed_prefill(p, Q.data_ptr(), K.data_ptr(), V.data_ptr(), cu_seqlens.data_ptr(),
-                                         cu_seqlens.numel() - 1, O.data_ptr(), lse.data_ptr() if lse is not None else None,
-                                         st), "dsa_packed_prefill")
+    if stream is not None or _current_device() != dev.index:
+        with _elsewhere(dev, stream):
+            return packed_prefill(Q, K, V, cu_seqlens, O, lse, want_lse)
+    st = _raw_stream(dev.index)
+    if O is None:
+        O = torch.empty_like(Q, memory_format=torch.contiguous_format)
+    lse = _lse(lse, want_lse, (Hq, T), dev)
+    if T > 0 and Hq > 0:
+        p = B.dsa_problem(Hq, Hkv, T, d, 64, 0, *_strides(Q), *_strides(K), *_strides(V), *_strides(O))
+        B.check(B.dsa_packed_prefill(p, Q.data_ptr(), K.data_ptr(), V.data_ptr(), cu_seqlens.data_ptr(),
+                                     cu_seqlens.numel() - 1, O.data_ptr(), lse.data_ptr() if lse is not None else None,
+                                     st), "dsa_packed_prefill")
     return O, lse
 
 
@@ -234,14 +223,17 @@ def build_tables(lens, new_lens, free_pages, free_count, block_table, page, max_
         _ints("out.cu_seqlens", out.cu_seqlens, (n + 1,), dev)
         _ints("out.lens", out.lens, (n,), dev)
         _ints("out.free_count", out.free_count, (1,), dev)
-    with _on(dev, stream) as st:
-        if out is None:
-            new = torch.empty(max_tokens + 2 * n + 2, dtype=torch.int32, device=dev)
-            out = Tables(*new.split([max_tokens, n + 1, n, 1]))  # one allocation
-        B.check(B.lib().dsa_build_tables(
-            n, lens.data_ptr(), new_lens.data_ptr(), free_pages.data_ptr(), free_pages.numel(), free_count.data_ptr(),
-            block_table.data_ptr(), width, page, max_tokens, out.slots.data_ptr(),
-            out.cu_seqlens.data_ptr(), out.lens.data_ptr(), out.free_count.data_ptr(), st), "dsa_build_tables")
+    if stream is not None or _current_device() != dev.index:
+        with _elsewhere(dev, stream):
+            return build_tables(lens, new_lens, free_pages, free_count, block_table, page, max_tokens, out)
+    st = _raw_stream(dev.index)
+    if out is None:
+        new = torch.empty(max_tokens + 2 * n + 2, dtype=torch.int32, device=dev)
+        out = Tables(*new.split_with_sizes([max_tokens, n + 1, n, 1]))  # one allocation
+    B.check(B.lib().dsa_build_tables(
+        n, lens.data_ptr(), new_lens.data_ptr(), free_pages.data_ptr(), free_pages.numel(), free_count.data_ptr(),
+        block_table.data_ptr(), width, page, max_tokens, out.slots.data_ptr(),
+        out.cu_seqlens.data_ptr(), out.lens.data_ptr(), out.free_count.data_ptr(), st), "dsa_build_tables")
     return out
 
 
@@ -257,9 +249,12 @@ def cache_write(K, V, slots, cache, stream=None):
     _ints("slots", slots, (T,), dev)
     if T == 0:
         return
-    with _on(dev, stream) as st:
-        B.check(B.lib().dsa_cache_write(ctypes.byref(c), K.data_ptr(), V.data_ptr(), *_strides(K), *_strides(V),
-                                        slots.data_ptr(), T, st), "dsa_cache_write")
+    if stream is not None or _current_device() != dev.index:
+        with _elsewhere(dev, stream):
+            return cache_write(K, V, slots, cache)
+    st = _raw_stream(dev.index)
+    B.check(B.lib().dsa_cache_write(ctypes.byref(c), K.data_ptr(), V.data_ptr(), *_strides(K), *_strides(V),
+                                    slots.data_ptr(), T, st), "dsa_cache_write")
 
 
 def cache_attention(Q, cache, block_table, lens, n_q=1, O=None, lse=None, want_lse=False, workspace=None, stream=None):
@@ -287,17 +282,20 @@ def cache_attention(Q, cache, block_table, lens, n_q=1, O=None, lse=None, want_l
     if workspace is not None:
         if workspace.device != dev or not workspace.is_contiguous() or workspace.nbytes < need:
             _refuse(f"workspace must hold {need} bytes on {dev}")
-    with _on(dev, stream) as st:
-        if O is None:
-            O = torch.empty_like(Q, memory_format=torch.contiguous_format)
-        lse = _lse(lse, want_lse, (Hq, T), dev)
-        if workspace is None:
-            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-        if n > 0:
-            B.check(B.lib().dsa_cache_attention(
-                ctypes.byref(c), Q.data_ptr(), Hq, *_strides(Q), block_table.data_ptr(), width, lens.data_ptr(), n, n_q,
-                O.data_ptr(), *_strides(O), lse.data_ptr() if lse is not None else None, workspace.data_ptr(),
-                workspace.nbytes, st), "dsa_cache_attention")
+    if stream is not None or _current_device() != dev.index:
+        with _elsewhere(dev, stream):
+            return cache_attention(Q, cache, block_table, lens, n_q, O, lse, want_lse, workspace)
+    st = _raw_stream(dev.index)
+    if O is None:
+        O = torch.empty_like(Q, memory_format=torch.contiguous_format)
+    lse = _lse(lse, want_lse, (Hq, T), dev)
+    if workspace is None:
+        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+    if n > 0:
+        B.check(B.lib().dsa_cache_attention(
+            ctypes.byref(c), Q.data_ptr(), Hq, *_strides(Q), block_table.data_ptr(), width, lens.data_ptr(), n, n_q,
+            O.data_ptr(), *_strides(O), lse.data_ptr() if lse is not None else None, workspace.data_ptr(),
+            workspace.nbytes, st), "dsa_cache_attention")
     return O, lse
 
 
