@@ -26,8 +26,8 @@
 //     (4860 cycles), and the issuing thread was busy for 2700 of them;
 //   halves of 64 keys with one thread issuing: 12.8 ms (issue-bound); descriptors as uniform values of a
 //     whole warp, one lane elected: 10.0 ms; a warp for each tile: 8.1 ms.
-//   For d 64, where the softmax is the bound, 5 of 16 exponentials as polynomials: 0.269 -> 0.235 ms
-//     (16 heads, 8192 tokens); for d 128 that changes nothing.
+//   Part of the exponentials as polynomials on the multiply-add pipe, spread between the others: d 64 (16 heads,
+//     8192 tokens) 0.269 -> 0.234 ms with 5 of 16, d 128 (32768 tokens) 8.33 -> 8.13 ms with 4 of 16.
 // V FIX: a hidden key has P = 0, but 0 x infinity is NaN.  The last key tile of a row tile holds
 // rows behind the sequence's end (another request's values) and keys that some rows must not
 // see; warps 11-14 zero the former, and zero the non-finite elements of the others, noting
@@ -140,11 +140,8 @@ template <int D>
 __global__ void __launch_bounds__(PACK_THREADS, 1)
 packed_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                    const __grid_constant__ CUtensorMap tmV, const __grid_constant__ PackArgs a) {
-  pdl_prologue();
   using L = PackSmem<D>;
   constexpr int DS = L::DS, NST = L::NST;
-  // of 16 pairs of weights, those whose exponentials are polynomials (see the measurements above)
-  constexpr int POLY = D == 64 ? 5 : 0;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint64_t* bars = reinterpret_cast<uint64_t*>(sm + L::BAR_OFF);
@@ -165,14 +162,16 @@ packed_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
     fence_barrier_init();
     misc[2] = 0;
   }
-  if (warp == 9) {
-    tmem_alloc(reinterpret_cast<uint32_t*>(&misc[0]), PACK_TMEM);
-    tc_fence_before();
-  }
   if (warp == 8 && lane == 0) {
     tma_prefetch_desc(&tmQ);
     tma_prefetch_desc(&tmK);
     tma_prefetch_desc(&tmV);
+  }
+  // Tensor memory is taken behind this wait only: the grid in front may still have to take its own.
+  pdl_prologue();
+  if (warp == 9) {
+    tmem_alloc(reinterpret_cast<uint32_t*>(&misc[0]), PACK_TMEM);
+    tc_fence_before();
   }
   __syncthreads();
   tc_fence_after();
@@ -546,7 +545,7 @@ packed_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
             float x0, x1;
             serve_fma2(s[32 * c + 2 * i], s[32 * c + 2 * i + 1], a.scale_log2, negm, x0, x1);
             float p0, p1;
-            if (i < POLY) {
+            if (D == 64 ? i % 3 == 1 : i % 4 == 1) {  // see the measurements above
               serve_ex2_poly2(x0, x1, p0, p1);
             } else {
               p0 = serve_ex2(x0);
