@@ -405,6 +405,10 @@ constexpr int AT_MAX_CTAS = 592;             // sizes the workspace
 // A CTA takes at least so many tiles.  One request of 1000 tokens, 8 KV heads: 10.3 us with 4 (32 CTAs), 12.9 with 3,
 // 14.0 with 6.
 constexpr int AT_MIN_TILES = 4;
+// A unit costs its tiles and this much for its start (pages, scales, Q): without it, CTAs whose range holds two units
+// end last.  32 requests of up to 8192 keys, 8 heads of d 128: 58 us, 79 without; 10 of up to 4000, 16 heads of d 64:
+// 19 and 33.
+constexpr int AT_START = 4;
 constexpr float P_OFF = 10.f, P_LAG = 5.f;
 // CTAs of an SM, with at_stages() ring stages each: what counts is the bytes on their way.  d 128, a million keys of 8
 // heads: 352 us with 3 CTAs of 4 stages, 409 with 2 of 6, 422 with 4 of 3.  d 64 (boxes half as large), 20 requests
@@ -438,10 +442,9 @@ struct AttendSmem {
   static constexpr int BOX = AT_KEYS * D;  // 16 rows of K or V
   static constexpr int RING = AT_WARPS * NST * 2 * BOX;
   static constexpr int JOIN = AT_WARPS * 16 * (D + 4) * 4;
-  static constexpr int SC = RING > JOIN ? RING : JOIN;         // float2 [warp][stage]: the scales, 0: no keys
-  static constexpr int BAR = SC + AT_WARPS * NST * 8;          // uint64 [warp][stage]
-  static constexpr int PRE = BAR + AT_WARPS * NST * 8;         // int [requests + 1]
-  static int bytes(int n_req) { return 1024 + PRE + (n_req + 1) * 4; }
+  static constexpr int BAR = RING > JOIN ? RING : JOIN;        // uint64 [warp][stage]
+  static constexpr int PRE = BAR + AT_WARPS * NST * 8;         // int [requests + 1], int [requests]
+  static int bytes(int n_req) { return 1024 + PRE + (2 * n_req + 1) * 4; }
 };
 
 // Box of 16 rows at (page, head, token) of K or V.
@@ -495,14 +498,19 @@ __device__ __forceinline__ int req_len(const AttendArgs& a, int b, bool tell) {
   return l;
 }
 
-// pre[b] = key tiles of the requests before b; returns their total.
-__device__ __forceinline__ int scan_tiles(const AttendArgs& a, int* pre, bool tell) {
+// pre[b] = the cost of a unit of each request before b, in key tiles; returns their total.  len_of: their lengths.
+__device__ __forceinline__ int scan_costs(const AttendArgs& a, int* pre, int* len_of, bool tell) {
   __shared__ int part[AT_WARPS];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   int base = 0;
   for (int b0 = 0; b0 < a.n_req; b0 += AT_THREADS) {
     const int b = b0 + tid;
-    const int c = b < a.n_req ? ceil_div(req_len(a, b, tell), AT_TILE) : 0;
+    int c = 0;
+    if (b < a.n_req) {
+      const int len = req_len(a, b, tell);
+      if (len_of != nullptr) len_of[b] = len;
+      c = len > 0 ? AT_START + ceil_div(len, AT_TILE) : 0;
+    }
     int v = c;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -571,7 +579,6 @@ k_cache_attend(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int g = lane >> 2, tq = lane & 3;
   uint8_t* ring = smem + warp * NST * 2 * L::BOX;
-  float2* scales = reinterpret_cast<float2*>(smem + L::SC) + warp * NST;
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + L::BAR) + warp * NST;
   if (tid == 0) abort_word = 0;
   if (lane == 0) {
@@ -582,9 +589,10 @@ k_cache_attend(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
       tma_prefetch_desc(&tmV);
     }
   }
-  pdl_prologue();
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   const int U = a.Hkv * a.MT;
-  const int total_req = scan_tiles(a, pre, blockIdx.x == 0);
+  int* const len_of = pre + a.n_req + 1;
+  const int total_req = scan_costs(a, pre, len_of, blockIdx.x == 0);
   const int64_t total = (int64_t)total_req * U;
 
   // requests without keys: every row is empty
@@ -599,9 +607,14 @@ k_cache_attend(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
     }
   }
   const int ctas = used_ctas(total, gridDim.x);
-  if (total == 0 || (int)blockIdx.x >= ctas) return;
+  if (total == 0 || (int)blockIdx.x >= ctas) return;  // (which lets the next grid begin as well)
   const Cut cut(total, ctas);
   const int64_t from = cut.first(blockIdx.x), to = cut.first(blockIdx.x + 1);
+  // The join's CTAs may come early where the work is short (one request of 1000 keys: 10.4 us instead of 11.4); where
+  // it is long they wait in places that this grid's successors want (128 requests of up to 4000 keys: 152 instead of
+  // 114 us).
+  const bool soon = cut.each <= 8;
+  if (soon) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   uint32_t phases = 0;  // bit: parity that the stage's next load completes
   uint32_t flying = 0;  // bit: the stage has a load that nobody has waited for
   bool dead = false;    // a wait ran out: nothing is loaded or computed from here on
@@ -609,72 +622,64 @@ k_cache_attend(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
   for (int64_t at = from; at < to;) {
     // the unit (request, KV head, row tile) that holds tile `at`
     const int b = owner_of(pre, a.n_req, (int)div_by(at, U));
-    const int tiles = pre[b + 1] - pre[b];
+    const int cost = pre[b + 1] - pre[b], tiles = cost - AT_START;
     const int64_t base = (int64_t)pre[b] * U;
-    const int unit = (int)div_by(at - base, tiles);
-    const int64_t unit0 = base + (int64_t)unit * tiles;
-    const int t0 = (int)(at - unit0);
+    const int unit = (int)div_by(at - base, cost);
+    const int64_t unit0 = base + (int64_t)unit * cost + AT_START;  // its first tile, behind what its start costs
+    const int t0 = (int)max((int64_t)0, at - unit0);
     const int t1 = (int)min((int64_t)tiles, to - unit0);
+    at = min(to, unit0 + tiles);
+    if (t1 <= t0) continue;
     const int kvh = unit / a.MT, mt = unit - kvh * a.MT;
-    const int len = req_len(a, b, false);
+    const int len = len_of[b];
     const int rows = a.n_q * a.G;
-    at = unit0 + t1;
 
     const int steps = t1 - t0;
     const int32_t* trow = a.table + (int64_t)b * a.width;
     // page numbers and scales of 32 steps at a time, one per lane
     auto load_page = [&](int i0) {
       const int key = (t0 + i0 + lane) * AT_TILE + warp * AT_KEYS;
-      return i0 + lane < steps && key < len ? trow[key >> a.shift] : -1;
+      if (i0 + lane >= steps || key >= len) return -1;
+      const int pg = trow[key >> a.shift];
+      return pg < 0 || pg >= a.num_pages ? -2 : pg;  // -2: a number that is none
     };
-    auto load_scales = [&](int i0, int& pg) {
-      float2 sc = make_float2(0.f, 0.f);
-      const int key = (t0 + i0 + lane) * AT_TILE + warp * AT_KEYS;
-      if (i0 + lane < steps && key < len) {
-        if (pg < 0 || pg >= a.num_pages) {
-          report(a.status, DSA_ERR_DEVICE, DETAIL_BAD_PAGE);
-          pg = -1;
-        } else {
-          sc = make_float2(a.k_scale[(int64_t)pg * a.Hkv + kvh], a.v_scale[(int64_t)pg * a.Hkv + kvh]);
-          if (!(good_scale(sc.x) && good_scale(sc.y))) {
-            report(a.status, DSA_ERR_DEVICE, DETAIL_BAD_SCALE);
-            sc = make_float2(0.f, 0.f);
-            pg = -1;
-          }
-        }
-      }
-      return sc;
+    auto load_scales = [&](int pg) {  // (checked where they are used)
+      return pg < 0 ? make_float2(0.f, 0.f)
+                    : make_float2(a.k_scale[(int64_t)pg * a.Hkv + kvh], a.v_scale[(int64_t)pg * a.Hkv + kvh]);
     };
     int page = load_page(0), page_next = load_page(32);
-    float2 sc = load_scales(0, page), sc_next = make_float2(0.f, 0.f);
+    float2 sc_next = make_float2(0.f, 0.f);
     int win = 0;   // steps whose pages `page` begins with
     int put = 0;   // stage of the next step to be loaded
     auto issue = [&](int i) {
       if (i < steps) {
-        const int at_lane = i - win;
-        const int pg = __shfl_sync(0xffffffffu, page, at_lane);
-        if (lane == at_lane) scales[put] = sc;
-        if (pg >= 0 && !dead) flying |= 1u << put;
-        if (pg >= 0 && !dead && lane == 0) {
-          uint8_t* dst = ring + put * 2 * L::BOX;
-          const int token = ((t0 + i) * AT_TILE + warp * AT_KEYS) & ((1 << a.shift) - 1);
-          mbar_arrive_expect_tx(&full[put], 2 * L::BOX);
-          tma_load_rows(dst, &tmK, &full[put], token, kvh, pg);
-          tma_load_rows(dst + L::BOX, &tmV, &full[put], token, kvh, pg);
+        const int pg = __shfl_sync(0xffffffffu, page, i - win);
+        if (pg >= 0 && !dead) {
+          flying |= 1u << put;
+          if (lane == 0) {
+            uint8_t* dst = ring + put * 2 * L::BOX;
+            const int token = ((t0 + i) * AT_TILE + warp * AT_KEYS) & ((1 << a.shift) - 1);
+            mbar_arrive_expect_tx(&full[put], 2 * L::BOX);
+            tma_load_rows(dst, &tmK, &full[put], token, kvh, pg);
+            tma_load_rows(dst + L::BOX, &tmV, &full[put], token, kvh, pg);
+          }
         }
-        if (at_lane == 15) sc_next = load_scales(win + 32, page_next);
-        if (at_lane == 31) {
+        if (i - win == 31) {  // the next 32 pages; their scales are wanted a few steps from here
           win += 32;
+          if (page_next == -2) report(a.status, DSA_ERR_DEVICE, DETAIL_BAD_PAGE);
           page = page_next;
-          sc = sc_next;
+          sc_next = load_scales(page);
           page_next = load_page(win + 32);
         }
       }
       put = put + 1 == NST ? 0 : put + 1;
     };
+    if (page == -2) report(a.status, DSA_ERR_DEVICE, DETAIL_BAD_PAGE);
 
 #pragma unroll 1
     for (int i = 0; i < NST - 1; ++i) issue(i);
+    float2 sc = load_scales(page);  // of this lane's step of the window that is computed
+    int swin = 0;
 
     // Q: row 8 n + g of the tile, this lane's 16-byte chunks, scaled by a power of two per row into fp16
     uint32_t qb[NQ][KS][2];
@@ -742,10 +747,14 @@ k_cache_attend(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
 #pragma unroll 1
     for (int i = 0; i < steps; ++i) {
       __syncwarp();
-      const float2 ss = scales[got];
+      if (i - swin == 32) {
+        swin += 32;
+        sc = sc_next;
+      }
+      const float2 ss = make_float2(__shfl_sync(0xffffffffu, sc.x, i - swin), __shfl_sync(0xffffffffu, sc.y, i - swin));
       const uint8_t* kp = ring + got * 2 * L::BOX;
       const uint8_t* vp = kp + L::BOX;
-      bool use = ss.x > 0.f && !dead;
+      bool use = ((flying >> got) & 1u) && !dead;
       if (use) {
         if (!serve_warp_wait(&full[got], (phases >> got) & 1u, a.wait_limit_ns, a.status, DETAIL_WAIT_K, abort_flag, true)) {
           dead = true;
@@ -753,6 +762,10 @@ k_cache_attend(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
         } else {
           phases ^= 1u << got;
           flying &= ~(1u << got);
+          if (!(good_scale(ss.x) && good_scale(ss.y))) {
+            if (lane == 0) report(a.status, DSA_ERR_DEVICE, DETAIL_BAD_SCALE);
+            use = false;
+          }
         }
       }
       if (use) {
@@ -988,6 +1001,7 @@ k_cache_attend(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
     fence_proxy_async_smem();
     __syncthreads();  // the ring may be filled again
   }
+  if (!soon) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 
 // Units that a range's end cut: adds their parts in range order.  A part of the unit's first tiles
@@ -998,17 +1012,17 @@ __global__ void __launch_bounds__(AT_THREADS) k_cache_join(const __grid_constant
   extern __shared__ int pre[];
   // the lengths were written before the kernel in front of this one began, so they can be read before it ends
   const int U = a.Hkv * a.MT;
-  const int64_t total = (int64_t)scan_tiles(a, pre, false) * U;
+  const int64_t total = (int64_t)scan_costs(a, pre, nullptr, false) * U;
   const int b = blockIdx.x / U, unit = blockIdx.x - b * U;
-  const int tiles = pre[b + 1] - pre[b];
-  const int64_t u0 = (int64_t)pre[b] * U + (int64_t)unit * tiles;
+  const int cost = pre[b + 1] - pre[b], tiles = cost - AT_START;
+  const int64_t u0 = (int64_t)pre[b] * U + (int64_t)unit * cost + AT_START;
   const Cut cut(max(total, (int64_t)1), used_ctas(total, grid));
   const int c0 = cut.holder(u0), c1 = cut.holder(u0 + max(tiles, 1) - 1);  // the CTAs with the unit's first and last tile
   const int kvh = unit / a.MT, mt = unit - kvh * a.MT;
   const int rows = min(16, a.n_q * a.G - mt * 16);
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  if (tiles == 0 || c0 == c1) return;
+  if (cost == 0 || c0 == c1) return;
   constexpr int TPR = D / 4;  // lanes of a row: 32 or 16
   const int lane = threadIdx.x & 31, sub = lane % TPR, c = sub * 4;
   // (whole warps: the rows are padded to a multiple of what a warp takes)
@@ -1228,7 +1242,7 @@ dsa_status dsa_cache_attention(const dsa_cache* cache, const void* Q, int32_t Hq
   if (width < 1) return DSA_ERR_INVALID_ARG;
   const int64_t most = (int64_t)width * cache->page;
   if (n_req > MAX_REQ || Hq > 4096 || n_q > 4096 || most > 0x7fffff00ll ||
-      (most / AT_TILE + 1) * n_req > 0x7fffffffll)
+      (most / AT_TILE + 1 + AT_START) * n_req > 0x7fffffffll)
     return DSA_ERR_UNSUPPORTED;
   if (!Q || !O || !block_table || !lens || !workspace) return DSA_ERR_INVALID_ARG;
   if (!serve_aligned16(Q) || !serve_aligned16(O) || !serve_aligned16(workspace)) return DSA_ERR_INVALID_ARG;
