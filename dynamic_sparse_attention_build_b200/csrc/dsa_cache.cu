@@ -402,8 +402,8 @@ constexpr int AT_WARPS = AT_THREADS / 32;
 constexpr int AT_KEYS = 16;                  // keys of a warp's step
 constexpr int AT_TILE = AT_KEYS * AT_WARPS;  // keys of a CTA's step
 constexpr int AT_MAX_CTAS = 592;             // sizes the workspace
-// A CTA takes at least so many tiles.  One request of 1000 tokens, 8 KV heads: 10.3 us with 4 (32 CTAs), 12.9 with 3,
-// 14.0 with 6.
+// A CTA takes at least so many tiles.  One request of 1000 tokens, 8 KV heads: 9.4 us with 4, 10.9 with 6, 12.4 with 8;
+// one of 96396 tokens, 1 KV head, whose parts are many: 24, 21 and 20.
 constexpr int AT_MIN_TILES = 4;
 // A unit costs its tiles and this much for its start (pages, scales, Q): without it, CTAs whose range holds two units
 // end last.  32 requests of up to 8192 keys, 8 heads of d 128: 58 us, 79 without; 10 of up to 4000, 16 heads of d 64:
@@ -411,7 +411,7 @@ constexpr int AT_MIN_TILES = 4;
 constexpr int AT_START = 4;
 constexpr float P_OFF = 10.f, P_LAG = 5.f;
 // CTAs of an SM, with at_stages() ring stages each: what counts is the bytes on their way.  d 128, a million keys of 8
-// heads: 352 us with 3 CTAs of 4 stages, 409 with 2 of 6, 422 with 4 of 3.  d 64 (boxes half as large), 20 requests
+// heads: 352 us with 3 CTAs of 4 stages, 409 with 2 of 6, 422 with 4 of 3 (333 now, 98% of a copy's rate).  d 64 (boxes half as large), 20 requests
 // of up to 4001 tokens, 16 heads: 37 us with 4 CTAs of 6 stages, 55 with 3 of 8.
 __host__ __device__ constexpr int at_per_sm(int d, int nq) { return d == 64 && nq == 1 ? 4 : 3; }
 __host__ __device__ constexpr int at_stages(int d) { return d == 128 ? 4 : 6; }
@@ -610,9 +610,9 @@ k_cache_attend(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
   if (total == 0 || (int)blockIdx.x >= ctas) return;  // (which lets the next grid begin as well)
   const Cut cut(total, ctas);
   const int64_t from = cut.first(blockIdx.x), to = cut.first(blockIdx.x + 1);
-  // The join's CTAs may come early where the work is short (one request of 1000 keys: 10.4 us instead of 11.4); where
-  // it is long they wait in places that this grid's successors want (128 requests of up to 4000 keys: 152 instead of
-  // 114 us).
+  // The join's CTAs may come early where the work is short (one request of 1000 keys: 10.4 us, 11.4 without); where
+  // it is long they wait in places that this grid's successors want (128 requests of up to 4000 keys: 152 us, 114
+  // without).
   const bool soon = cut.each <= 8;
   if (soon) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   uint32_t phases = 0;  // bit: parity that the stage's next load completes
@@ -1006,7 +1006,9 @@ k_cache_attend(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
 
 // Units that a range's end cut: adds their parts in range order.  A part of the unit's first tiles
 // is its CTA's last one (slot 1), every other part is its CTA's first (slot 0).
-// One lane per part for the maxima and sums, then one lane per 4 columns for O.
+// A unit may have as many parts as there are CTAs (one request with one KV head), so a CTA takes one row at a time: its
+// groups of D / 4 threads take parts in turn, 4 columns a thread, and meet in shared memory.  (With a warp for each
+// row, one request of 96396 keys, 1 KV head, took 121 us.)
 template <int D>
 __global__ void __launch_bounds__(AT_THREADS) k_cache_join(const __grid_constant__ AttendArgs a, int grid) {
   extern __shared__ int pre[];
@@ -1023,50 +1025,59 @@ __global__ void __launch_bounds__(AT_THREADS) k_cache_join(const __grid_constant
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (cost == 0 || c0 == c1) return;
-  constexpr int TPR = D / 4;  // lanes of a row: 32 or 16
-  const int lane = threadIdx.x & 31, sub = lane % TPR, c = sub * 4;
-  // (whole warps: the rows are padded to a multiple of what a warp takes)
-  const int per_warp = 32 / TPR;
-  for (int r0 = (blockIdx.y * AT_WARPS + (threadIdx.x >> 5)) * per_warp; r0 < rows; r0 += AT_WARPS * per_warp * gridDim.y) {
-    const int row = r0 + lane / TPR;
-    const bool in = row < rows;
+  constexpr int TPR = D / 4, GROUPS = AT_THREADS / TPR;
+  __shared__ float s_max[AT_WARPS];
+  __shared__ float s_sum[GROUPS];
+  __shared__ __align__(16) float s_acc[GROUPS][D];
+  const int tid = threadIdx.x, grp = tid / TPR, c = (tid % TPR) * 4;
+  const int n = c1 - c0 + 1;
+  for (int row = blockIdx.y; row < rows; row += gridDim.y) {
     auto part = [&](int k) {  // the unit's first part is its CTA's last one, every other its CTA's first
-      return a.part + ((int64_t)((c0 + k) * 2 + (k == 0 ? 1 : 0)) * 16 + (in ? row : 0)) * (D + 4);
+      return a.part + ((int64_t)((c0 + k) * 2 + (k == 0 ? 1 : 0)) * 16 + row) * (D + 4);
     };
-    const int n = c1 - c0 + 1;
     float M = -INFINITY;
-    for (int k = sub; k < n; k += TPR) M = fmaxf(M, part(k)[0]);
+    for (int k = tid; k < n; k += AT_THREADS) M = fmaxf(M, part(k)[0]);
+    M = warp_max(M);
+    if ((tid & 31) == 0) s_max[tid >> 5] = M;
+    __syncthreads();
 #pragma unroll
-    for (int o = TPR / 2; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+    for (int w = 0; w < AT_WARPS; ++w) M = fmaxf(M, s_max[w]);
     float acc[4] = {0.f, 0.f, 0.f, 0.f}, lsum = 0.f;
-    for (int k0 = 0; k0 < n; k0 += TPR) {
-      float f = 0.f;
-      if (k0 + sub < n) {
-        const float* w = part(k0 + sub);
-        f = w[0] == -INFINITY ? 0.f : serve_ex2(w[0] - M);
-        lsum += w[1] * f;
-      }
-      const int m = min(TPR, n - k0);
-#pragma unroll 8
-      for (int k = 0; k < m; ++k) {
-        const float4 v = *reinterpret_cast<const float4*>(part(k0 + k) + 4 + c);
-        const float fk = __shfl_sync(0xffffffffu, f, k, TPR);
-        acc[0] += v.x * fk;
-        acc[1] += v.y * fk;
-        acc[2] += v.z * fk;
-        acc[3] += v.w * fk;
-      }
+#pragma unroll 4
+    for (int k = grp; k < n; k += GROUPS) {
+      const float* w = part(k);
+      const float4 v = *reinterpret_cast<const float4*>(w + 4 + c);
+      const float f = w[0] == -INFINITY ? 0.f : serve_ex2(w[0] - M);
+      lsum += w[1] * f;
+      acc[0] += v.x * f;
+      acc[1] += v.y * f;
+      acc[2] += v.z * f;
+      acc[3] += v.w * f;
     }
+    *reinterpret_cast<float4*>(&s_acc[grp][c]) = make_float4(acc[0], acc[1], acc[2], acc[3]);
+    if (c == 0) s_sum[grp] = lsum;
+    __syncthreads();
+    if (tid < TPR) {
 #pragma unroll
-    for (int o = TPR / 2; o > 0; o >>= 1) lsum += __shfl_xor_sync(0xffffffffu, lsum, o);
-    if (!in) continue;
-    const RowAt ra = row_at(a, b, kvh, mt * 16 + row);
-    const float inv = lsum == 0.f ? 0.f : 1.f / lsum;
-    const __nv_bfloat162 v0 = __floats2bfloat162_rn(acc[0] * inv, acc[1] * inv), v1 = __floats2bfloat162_rn(acc[2] * inv, acc[3] * inv);
-    *reinterpret_cast<uint2*>(a.O + ra.head * a.o_hs + (int64_t)ra.token * a.o_ts + c) =
-        make_uint2(*reinterpret_cast<const uint32_t*>(&v0), *reinterpret_cast<const uint32_t*>(&v1));
-    if (c == 0 && a.lse != nullptr)
-      a.lse[(int64_t)ra.head * a.T + ra.token] = lsum == 0.f ? -INFINITY : (M - P_OFF + log2f(lsum)) * 0.69314718055994531f;
+      for (int i = 1; i < GROUPS; ++i) {
+        const float4 v = *reinterpret_cast<const float4*>(&s_acc[i][c]);
+        acc[0] += v.x;
+        acc[1] += v.y;
+        acc[2] += v.z;
+        acc[3] += v.w;
+      }
+      lsum = 0.f;
+#pragma unroll
+      for (int i = 0; i < GROUPS; ++i) lsum += s_sum[i];
+      const RowAt ra = row_at(a, b, kvh, mt * 16 + row);
+      const float inv = lsum == 0.f ? 0.f : 1.f / lsum;
+      const __nv_bfloat162 v0 = __floats2bfloat162_rn(acc[0] * inv, acc[1] * inv), v1 = __floats2bfloat162_rn(acc[2] * inv, acc[3] * inv);
+      *reinterpret_cast<uint2*>(a.O + ra.head * a.o_hs + (int64_t)ra.token * a.o_ts + c) =
+          make_uint2(*reinterpret_cast<const uint32_t*>(&v0), *reinterpret_cast<const uint32_t*>(&v1));
+      if (c == 0 && a.lse != nullptr)
+        a.lse[(int64_t)ra.head * a.T + ra.token] = lsum == 0.f ? -INFINITY : (M - P_OFF + log2f(lsum)) * 0.69314718055994531f;
+    }
+    __syncthreads();  // the places are free again
   }
 }
 
@@ -1125,9 +1136,9 @@ dsa_status launch_attend(const dsa_cache& c, AttendArgs& a, cudaStream_t stream)
   const int grid = min(at_per_sm(D, NQ) * sms, AT_MAX_CTAS);
   if (e == cudaSuccess) e = launch_pdl(k_cache_attend<D, NQ>, dim3(grid), dim3(AT_THREADS), (size_t)smem, stream, mk, mv, a);
   const int rows = min(16, a.n_q * a.G);
-  const int per_unit = ceil_div(rows * (D / 4), AT_THREADS);
+  const int units = a.n_req * a.Hkv * a.MT, per_unit = max(1, min(rows, 2048 / units));  // a CTA a row while CTAs are few
   if (e == cudaSuccess)
-    e = launch_pdl(k_cache_join<D>, dim3(a.n_req * a.Hkv * a.MT, per_unit), dim3(AT_THREADS), (size_t)(a.n_req + 1) * 4, stream, a, grid);
+    e = launch_pdl(k_cache_join<D>, dim3(units, per_unit), dim3(AT_THREADS), (size_t)(a.n_req + 1) * 4, stream, a, grid);
   if (e == cudaSuccess) e = cudaGetLastError();
   return e == cudaSuccess ? DSA_OK : cuda_fail(e);
 }

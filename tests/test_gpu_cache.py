@@ -277,6 +277,8 @@ CASES = [
     (8, 1, 64, 256, [700, 255], 1), (16, 1, 128, 16, [90, 33], 1), (16, 2, 64, 64, [200, 3, 0, 65], 5),
     (32, 1, 128, 64, [130, 20], 3), (2, 2, 64, 16, [4, 2, 9, 0], 7), (32, 8, 128, 64, [2111, 640], 2),
     (6, 2, 128, 32, [5000], 1), (4, 4, 64, 16, [1, 2, 3] * 60, 1), (8, 2, 128, 64, [3000], 40),
+    # a unit in as many parts as there are CTAs, rows of several tiles
+    (3, 1, 64, 32, [60000], 1), (32, 1, 128, 64, [20000, 5], 3), (2, 2, 128, 16, [1, 70000, 300], 1),
 ]
 
 
