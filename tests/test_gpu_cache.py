@@ -413,18 +413,27 @@ def test_attention_gives_the_same_bits_each_time(dsa):
 
 def test_waits_that_run_out_leave_the_next_launch_exact(dsa):
     from dynamic_sparse_attention_build_b200 import _binding as B
-    lens = [60000, 17, 50000, 70000]  # enough to fill the memory's bandwidth: loads take a few us
+    lens = [60000, 17, 50000, 70000]
     cache, table, dl, Q = attend_inputs(dsa, 8, 8, 128, 64, lens, 1)
+    src, side = torch.zeros(1 << 30, dtype=torch.uint8, device="cuda"), torch.cuda.Stream()
+    dst = torch.empty_like(src)  # copies beside the calls below, so that loads take long
     want, want_lse = dsa.cache_attention(Q, cache, table, dl, want_lse=True)
     assert dsa.device_status() == (0, 0)
     out = 0
     try:
-        for limit in (100, 300, 1000, 3000):
+        for limit in (1, 100, 300, 1000) * 5:
+            if out > 1:
+                break
             assert B.dsa_set_wait_limit(limit) == B.DSA_OK
-            dsa.cache_attention(Q, cache, table, dl)
+            with torch.cuda.stream(side):
+                for _ in range(4):
+                    dst.copy_(src)
+            for _ in range(3):
+                dsa.cache_attention(Q, cache, table, dl)
             status, _ = dsa.device_status()
             assert status in (B.DSA_OK, B.DSA_ERR_TIMEOUT)
             out += status == B.DSA_ERR_TIMEOUT
+            torch.cuda.synchronize()
     finally:
         assert B.dsa_set_wait_limit(0) == B.DSA_OK
     assert out > 0

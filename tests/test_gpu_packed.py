@@ -231,7 +231,7 @@ def test_waits_that_run_out_leave_the_next_launch_exact(dsa):
     assert dsa.device_status() == (0, 0)
     out = 0
     try:
-        for limit in (300, 1000, 3000, 10000):
+        for limit in (1, 300, 1000, 3000, 10000):
             assert B.dsa_set_wait_limit(limit) == B.DSA_OK
             dsa.packed_prefill(Q, K, V, cu)
             status, _ = dsa.device_status()
