@@ -36,7 +36,8 @@ __device__ __forceinline__ int owner_of(const int* pre, int n, int i) {
 // search).  Nothing is read that the call writes: a taken page is looked up where it comes from, the old stack or the
 // row of the request that gave it back; pushes go behind the old stack, takes behind a row's old pages.  So no step
 // waits for another, but for one case: where lengths or count are updated in place, one cluster does all the work,
-// and its barrier stands between their reads and writes.
+// and its barrier stands between their reads and writes.  200K slots of 48 prompts: 4.7 us (17.3 as one cluster with
+// barriers between the steps); 256 requests of one token: 7 to 9 us.
 // ---------------------------------------------------------------------------
 constexpr int TAB_THREADS = 512;
 
@@ -206,7 +207,8 @@ __global__ void __launch_bounds__(TAB_THREADS, 1) k_build_tables(const __grid_co
 // and no precision (e4m3 is relative), makes the scaling exact and lets older values move to a
 // larger scale without a second error unless they become subnormal.
 // Bound by memory: 2 bytes read and 1 written per element; a page's rows stay in registers between
-// the maximum and the rounding.
+// the maximum and the rounding.  71K tokens of 16 prompts, 8 heads of d 128: 77 us, 86% of a copy's rate; one token
+// for each of 64 requests: 5.3 us.
 // ---------------------------------------------------------------------------
 constexpr int ST_THREADS = 128;
 constexpr int ST_KEEP = 8;  // passes whose rows stay in registers (64 rows at d = 128)
@@ -1227,7 +1229,8 @@ dsa_status dsa_cache_write(const dsa_cache* cache, const void* K, const void* V,
   a.Hkv = cache->Hkv;
   a.shift = log2_page(cache->page);
   a.num_pages = cache->num_pages;
-  // a token a CTA while CTAs are few (each may be a run of its own), up to 128 once there are enough for every SM
+  // A token a CTA while CTAs are few (each may be a run of its own), up to 128 once there are enough for every SM.
+  // 64 tokens of 64 requests, 8 heads: 5.3 us with 1, 23 with 16, 82 with 128; 71K tokens of 16 prompts: 1177, 107 and 77.
   int chunk = 1;
   while (chunk < ST_THREADS && (int64_t)n_tokens * cache->Hkv * 2 > (int64_t)chunk * 4096) chunk *= 2;
   a.chunk = chunk;
@@ -1293,6 +1296,7 @@ dsa_status dsa_cache_attention(const dsa_cache* cache, const void* Q, int32_t Hq
   a.scale_log2 = (float)(1.4426950408889634 / sqrt((double)cache->d));
   a.status = st;
   a.wait_limit_ns = wait_limit_ns();
+  // (one n8 tile where it holds all rows: 64 ragged requests of 4 query heads a KV head 191 us, 272 with two)
   const bool one = n_q * a.G <= 8;
   if (cache->d == 128) return one ? launch_attend<128, 1>(*cache, a, (cudaStream_t)stream) : launch_attend<128, 2>(*cache, a, (cudaStream_t)stream);
   return one ? launch_attend<64, 1>(*cache, a, (cudaStream_t)stream) : launch_attend<64, 2>(*cache, a, (cudaStream_t)stream);

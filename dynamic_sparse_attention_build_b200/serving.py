@@ -304,8 +304,9 @@ class PagedLayer:
     tables, lengths and free pages, and the 8-bit cache of ``pages`` pages of ``page`` tokens.
     A request may hold ``width`` pages at most.  ``prefill`` takes prompts, short ones packed or
     one long one with sparse patterns, ``decode`` the tokens that follow.  Both enqueue work on
-    the current stream only, update lengths, tables and cache in place, and can be captured into
-    a CUDA graph.  Use it on one stream at a time.  If pages run out, no token of that call is
+    the current stream only and update lengths, tables and cache in place; ``decode``, and
+    ``prefill`` without patterns, can be captured into a CUDA graph.  Use it on one stream at a
+    time.  If pages run out, no token of that call is
     stored and ``status`` says DSA_ERR_CAPACITY."""
 
     def __init__(self, Hq, Hkv, d, requests, pages, page=64, width=None, device="cuda"):

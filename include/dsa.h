@@ -270,9 +270,9 @@ dsa_status dsa_set_wait_limit(uint64_t limit_ns);
  * ------------------------------------------------------------------------- */
 
 /* Dense causal attention over packed sequences.  Q [Hq], K and V [Hkv] hold N packed
- * rows (p->block is not used); rows cu_seqlens[s] .. cu_seqlens[s + 1] - 1 are sequence
- * s, n_seq of them (device int32 [n_seq + 1], ascending, 0 <= cu <= N; lengths of 0 are
- * fine).  Row i of a sequence attends to that sequence's rows j <= i:
+ * rows (p->block plays no part, but has to be one of its values); rows cu_seqlens[s] ..
+ * cu_seqlens[s + 1] - 1 are sequence s, n_seq of them (device int32 [n_seq + 1],
+ * ascending, 0 <= cu <= N; lengths of 0 are fine).  Row i of a sequence attends to that sequence's rows j <= i:
  *   O_i = sum_j softmax_j(q_i . k_j / sqrt(d)) v_j.
  * Values that a row must not see never reach it, infinities and NaN among them.
  * O: device bf16 with the problem's o strides; lse: optional device float [Hq * N].
