@@ -291,8 +291,10 @@ packed_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
         }
         ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
       }
-      // after an abort no load may still be on its way into shared memory when the CTA ends
-      if (lane == 0 && *abort_flag) {
+      // No load may still be on its way into shared memory when the CTA ends.  Whether another warp gives up before the
+      // last ones have landed is not known here, so this warp always waits for them: nothing arms these barriers again,
+      // and it has nothing else to do.
+      if (lane == 0) {
         if (q_last >= 0) serve_drain(&bars[L::QFULL], q_last & 1);
         for (uint32_t g = gs > NST ? gs - NST : 0; g < gs; ++g) serve_drain(&bars[L::FULL + g % NST], (g / NST) & 1);
       }

@@ -1,0 +1,42 @@
+"""No TMA load may be on its way into a CTA's shared memory when the CTA ends: the next CTA on
+that SM may own the memory by then.  Whether one still is after a wait ran out depends on when
+the other warps give up, which no run shows for sure and none may try on the GPU, so the kernels'
+source is read here (CPU): a loader that alone arms its barriers waits for its last loads whatever
+became of the others, and one that shares them leaves it to the CTA's end, when every warp has
+stopped and the abort flag is final."""
+import os
+import re
+
+CSRC = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "dynamic_sparse_attention_build_b200", "csrc")
+
+
+def source(name):
+    """The file without comments."""
+    text = open(os.path.join(CSRC, name), encoding="utf-8").read()
+    return re.sub(r"//[^\n]*|/\*.*?\*/", "", text, flags=re.S)
+
+
+def conditions_of(text, at):
+    """The heads of the blocks that hold position `at`, innermost first, up to the function's own."""
+    heads, depth = [], 0
+    for i in range(at - 1, -1, -1):
+        if text[i] == "}":
+            depth += 1
+        elif text[i] == "{":
+            if depth:
+                depth -= 1
+                continue
+            start = max(text.rfind(c, 0, i) for c in ";{}")
+            heads.append(" ".join(text[start + 1:i].split()))
+    return heads
+
+
+def statement(text, at):
+    return " ".join(text[max(text.rfind(c, 0, at) for c in "{};") + 1:at].split())
+
+
+def test_packed_prefill_waits_for_its_last_loads():
+    text = source("dsa_pack.cu")
+    at = text.index("serve_drain(&bars[L::QFULL]")
+    assert "serve_drain(&bars[L::FULL" in text[at:at + 400]
+    assert not any("abort" in c for c in conditions_of(text, at)[:2] + [statement(text, at)])

@@ -272,3 +272,31 @@ def test_misaligned_rows_are_refused(dsa):
     with pytest.raises(B.DSAError) as e:
         dsa.packed_prefill(Q, torch.zeros(2, 50, 65, dtype=torch.bfloat16, device="cuda")[:, :, 1:], V, ints([0, 50]))
     assert e.value.status == B.DSA_ERR_INVALID_ARG
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("lens", [[1], [128], [200, 250], [60, 1, 256] * 20])
+def test_waits_that_run_out_on_short_prompts(dsa, lens, d):
+    """Prompts whose loads are all on their way before the first wait ends: the loader never meets a wait of its own,
+    so another warp gives up first.  The launches behind the ones that gave up are exact."""
+    from dynamic_sparse_attention_build_b200 import _binding as B
+    Q, K, V = make(4, 2, sum(lens), d)
+    cu = ints(cu_of(lens))
+    want, want_lse = dsa.packed_prefill(Q, K, V, cu, want_lse=True)
+    assert dsa.device_status() == (0, 0)
+    out = 0
+    try:
+        for limit in (1, 100, 300, 1000, 3000):
+            assert B.dsa_set_wait_limit(limit) == B.DSA_OK
+            for _ in range(4):
+                dsa.packed_prefill(Q, K, V, cu)
+            assert B.dsa_set_wait_limit(0) == B.DSA_OK
+            O, lse = dsa.packed_prefill(Q, K, V, cu, want_lse=True)  # right behind them
+            status, _ = dsa.device_status()
+            assert status in (B.DSA_OK, B.DSA_ERR_TIMEOUT)
+            out += status == B.DSA_ERR_TIMEOUT
+            assert torch.equal(O, want) and torch.equal(lse, want_lse)
+    finally:
+        assert B.dsa_set_wait_limit(0) == B.DSA_OK
+    assert out > 0  # (a bound of 1 ns is shorter than any load)
+    assert dsa.device_status() == (0, 0)
