@@ -1067,27 +1067,23 @@ k_vs_tc(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtenso
                         i0 + r * 64, h);
       }
       int last[2] = {-1, -1};
-      bool ok = true;
       for (int t = 0; t < nsub; ++t) {
         const int b = t & 1;
         if (t >= 2 && !mbar_wait_ool(&bars[VB_KEMPTY + b], ((t >> 1) - 1) & 1, limit, status, DETAIL_WAIT_EMPTY,
-                                     abort_flag, true)) {
-          ok = false;
+                                     abort_flag, true))
           break;
-        }
         mbar_arrive_expect_tx(&bars[VB_KFULL + b], DS * VT_SLAB);
         last[b] = t;
         for (int c = 0; c < DS; ++c)
           tma_load_3d(sm + S::K_OFF + (b * DS + c) * VT_SLAB, &tmK, &bars[VB_KFULL + b], c * 64,
                       j0 + t * VT_ROWS, kvh);
       }
-      if (!ok) {
-        // a wait ran out: the loads this thread issued land before the CTA exits
-        // (only this thread arms these barriers, so the parities are unambiguous)
-        mbar_drain(&bars[VB_QFULL], 0);
-        for (int b = 0; b < 2; ++b)
-          if (last[b] >= 0) mbar_drain(&bars[VB_KFULL + b], (last[b] >> 1) & 1);
-      }
+      // The loads this thread issued land before the CTA exits, whichever warp's
+      // wait runs out, and when (only this thread arms these barriers, so the
+      // parities are unambiguous).
+      mbar_drain(&bars[VB_QFULL], 0);
+      for (int b = 0; b < 2; ++b)
+        if (last[b] >= 0) mbar_drain(&bars[VB_KFULL + b], (last[b] >> 1) & 1);
     }
     __syncwarp();
   } else if (warp == 1) {

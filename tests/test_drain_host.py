@@ -40,3 +40,10 @@ def test_packed_prefill_waits_for_its_last_loads():
     at = text.index("serve_drain(&bars[L::QFULL]")
     assert "serve_drain(&bars[L::FULL" in text[at:at + 400]
     assert not any("abort" in c for c in conditions_of(text, at)[:2] + [statement(text, at)])
+
+
+def test_vs_estimate_waits_for_its_last_loads():
+    text = source("dsa_index.cu")
+    at = text.index("mbar_drain(&bars[VB_QFULL]")
+    assert "mbar_drain(&bars[VB_KFULL" in text[at:at + 200]
+    assert conditions_of(text, at)[:2] == ["if (lane == 0)", "if (warp == 0)"] and statement(text, at) == ""
