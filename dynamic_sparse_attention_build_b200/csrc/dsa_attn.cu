@@ -342,16 +342,17 @@ static __device__ __noinline__ void mbar_drain(uint64_t* bar, uint32_t parity) {
   }
 }
 
-// After an abort, the producer drains its loads still in flight.  The MMA
-// thread records how far it has seen K, V and Q land (misc[11], [12], [13]); a
-// load it has not seen may still be in flight, and no later phase of that
-// buffer's barrier can have completed (filling the buffer again needs the load
-// consumed first), so the parity wait is unambiguous.
-static __device__ __noinline__ void drain_loads(uint64_t* bars, const int* misc, int q_kc, int pk0, int pk1,
-                                                int pv0, int pv1) {
+// After an abort, once every warp has stopped, the loads still in flight are
+// waited for.  The producer left what it issued last (misc[4] Q, [5], [6] K and
+// [7], [8] V per buffer), the MMA thread how far it has seen K, V and Q land
+// (misc[11], [12], [13]); a load it has not seen may still be in flight, and no
+// later phase of that buffer's barrier can have completed (filling the buffer
+// again needs the load consumed first), so the parity wait is unambiguous.
+static __device__ __noinline__ void drain_loads(uint64_t* bars, const int* misc) {
   const volatile int* vm = misc;
+  const int q_kc = vm[4];
   if (q_kc >= 0 && vm[13] <= q_kc) mbar_drain(&bars[B_QFULL], q_kc & 1);
-  const int pk[2] = {pk0, pk1}, pv[2] = {pv0, pv1};
+  const int pk[2] = {vm[5], vm[6]}, pv[2] = {vm[7], vm[8]};
   for (int b = 0; b < 2; ++b) {
     if (pk[b] >= 0 && vm[11] <= pk[b]) mbar_drain(&bars[B_KFULL + b], (pk[b] >> 1) & 1);
     if (pv[b] >= 0 && vm[12] <= pv[b]) mbar_drain(&bars[B_VFULL + b], (pv[b] >> 1) & 1);
@@ -405,7 +406,8 @@ sparse_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint64_t* bars = reinterpret_cast<uint64_t*>(sm + L::BAR_OFF);
   int* misc = reinterpret_cast<int*>(sm + L::MISC_OFF);
-  // misc: [0] tmem base, [2] abort, [3] unit count, [9] decoder go flag, [10] current item,
+  // misc: [0] tmem base, [2] abort, [3] unit count, [4] .. [8] the producer's last loads, [9] decoder go flag,
+  //       [10] current item,
   //       [11] / [12] K / V tiles the MMA thread has seen land, [13] items whose Q it has seen land
   volatile int* abort_flag = misc + 2;
   uint32_t* bits = reinterpret_cast<uint32_t*>(sm + L::BITS_OFF);  // [set][half][nwords]
@@ -538,7 +540,12 @@ sparse_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
         if (!ok) break;
         mbar_arrive(&bars[B_UNITS]);  // this item's bitmaps are no longer read here
       }
-      if (*abort_flag) drain_loads(bars, misc, q_kc, pk[0], pk[1], pv[0], pv[1]);
+      // for the teardown, which knows whether any warp's wait ran out
+      misc[4] = q_kc;
+      misc[5] = pk[0];
+      misc[6] = pk[1];
+      misc[7] = pv[0];
+      misc[8] = pv[1];
     }
     __syncwarp();
   } else if (warp == 2 || warp == 3) {
@@ -1104,6 +1111,9 @@ sparse_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
     tc_fence_after();
     tmem_dealloc(tmem_base, TMEM_COLS);
   }
+  // Every warp has stopped: without an abort each load has been consumed, after one
+  // the last ones may still be on their way.
+  if (tid == 0 && *abort_flag) drain_loads(bars, misc);
 }
 
 // --------------------------------------------------------------------------

@@ -47,3 +47,14 @@ def test_vs_estimate_waits_for_its_last_loads():
     at = text.index("mbar_drain(&bars[VB_QFULL]")
     assert "mbar_drain(&bars[VB_KFULL" in text[at:at + 200]
     assert conditions_of(text, at)[:2] == ["if (lane == 0)", "if (warp == 0)"] and statement(text, at) == ""
+
+
+def test_sparse_attention_waits_for_its_last_loads_when_every_warp_has_stopped():
+    """The decoders arm the same barriers for column tiles, so a parity only tells when nobody goes on."""
+    text = source("dsa_attn.cu")
+    body = text[text.index("sparse_attn_kernel(const __grid_constant__"):text.index("\nconstexpr int kSchedSlots")]
+    calls = [m.start() for m in re.finditer(r"drain_loads\(", body)]
+    assert len(calls) == 1 and calls[0] > body.rindex("__syncthreads();")
+    assert conditions_of(body, calls[0])[0].startswith("sparse_attn_kernel(") or "abort_flag" in conditions_of(body, calls[0])[0]
+    for name in ("q_kc", "pk[0]", "pk[1]", "pv[0]", "pv[1]"):  # the loader leaves what it has issued, on every way out
+        assert re.search(r"misc\[\d+\] = " + re.escape(name) + ";", body), name
