@@ -17,8 +17,11 @@
 //     P overwrites the first 32 columns of its half as bf16 pairs.  A half's next S = Q K^T goes
 //     out right behind its P V, while the softmax works on the other half;
 //   * the running maximum is raised only when it grows by more than 2^8, so O is rescaled almost
-//     never: a row's weights may be up to 2^8 instead of 1, relative roundings are the same, and
-//     l <= 2^29 and O <= 2^29 |V| stay inside fp32.
+//     never.  Weights are 2^(x - m - 8), at most 1 however far m lags: relative roundings are the
+//     same, l is at most the number of keys, and O stays inside fp32 wherever it would with an exact
+//     maximum (|V| below 2^128 / keys).  With weights up to 2^8, one key of 2^7.9 and a value of
+//     2^121 were infinite.  What it costs is at the other end: the largest weight may be 2^-8, so
+//     sums lose what is under 2^-118.
 // What bounds it: MMA operands and TMA together move about 320 KB of shared memory per 128 keys of an
 // item (2500 cycles at 128 bytes), the weights' exponentials take 2048 (16 a cycle); a step of 128
 // keys takes 3650 at 32K tokens.  Steps that led here (32 query heads on 8, d 128, one sequence of 32768):
@@ -52,7 +55,7 @@ constexpr int NITEM = 4;            // ItemInfo ring
 // Barriers for cleaned V tiles, used in turn.  One MMA warp may be up to two cleaned tiles ahead of the other: it
 // cannot pass the next item's Q before the other has issued all of this item's Q K^T, and an item has two of them.
 constexpr int NFIX = 4;
-constexpr float PACK_RESCALE = 8.0f;
+constexpr float PACK_RESCALE = 8.0f;  // how far (log2) a row's maximum may lag
 
 struct PackArgs {
   int Hq, G, T, nseq, npairs;
@@ -491,7 +494,7 @@ packed_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
       if (im->start < 0) break;
       const int n = im->n[x], start = im->start, row = im->row0[x] + r, h = im->h[x];
       const bool in = n > 0 && row < im->len;
-      float m = -INFINITY, l = 0.f;
+      float m = -INFINITY, l = 0.f;  // m: the running maximum when it was last raised, plus PACK_RESCALE
 #pragma unroll 1
       for (int u = 0; u < 2 * n; ++u) {
         const int half = u & 1;
@@ -512,10 +515,11 @@ packed_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
         float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
         for (int c = 0; c < TH / 2; ++c) mx[c & 3] = serve_max3(mx[c & 3], s[2 * c], s[2 * c + 1]);
-        const float m_new = fmaxf(m, fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * a.scale_log2);
+        const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * a.scale_log2;
         float alpha = 1.f;
         bool need = false;
-        if (m_new > m + PACK_RESCALE) {
+        if (top > m) {
+          const float m_new = top + PACK_RESCALE;
           if (m != -INFINITY) {
             alpha = serve_ex2(m - m_new);
             l *= alpha;

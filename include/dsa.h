@@ -274,7 +274,8 @@ dsa_status dsa_set_wait_limit(uint64_t limit_ns);
  * cu_seqlens[s + 1] - 1 are sequence s, n_seq of them (device int32 [n_seq + 1],
  * ascending, 0 <= cu <= N; lengths of 0 are fine).  Row i of a sequence attends to that sequence's rows j <= i:
  *   O_i = sum_j softmax_j(q_i . k_j / sqrt(d)) v_j.
- * Values that a row must not see never reach it, infinities and NaN among them.
+ * Values that a row must not see never reach it, infinities and NaN among them.  Sums of
+ * weights (at most 1) times values are held in fp32: n keys of |v| < 2^128 / n stay finite.
  * O: device bf16 with the problem's o strides; lse: optional device float [Hq * N].
  * Rows of no sequence (behind the last, say) are left as they were.  A sequence whose
  * bounds are malformed is skipped and reported as DSA_ERR_DEVICE.  A head stride of 0

@@ -300,3 +300,21 @@ def test_waits_that_run_out_on_short_prompts(dsa, lens, d):
         assert B.dsa_set_wait_limit(0) == B.DSA_OK
     assert out > 0  # (a bound of 1 ns is shorter than any load)
     assert dsa.device_status() == (0, 0)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("G", [1, 2])
+@pytest.mark.parametrize("power", [119, 121])
+def test_large_values_under_a_maximum_that_lags(dsa, G, d, power):
+    """The row's first keys weigh 1, a later one 2^7.9 with a value near the type's largest: a maximum that is not
+    raised for it must not take the sum out of fp32's range, as it would stay in it with an exact maximum."""
+    T = 300
+    Q, K = torch.zeros(G, T, d, dtype=torch.bfloat16, device="cuda"), torch.zeros(1, T, d, dtype=torch.bfloat16, device="cuda")
+    V = make(G, 1, T, d)[2]
+    Q[:, :, 0] = 8.0
+    for at in (100, 170):  # in the half tile and in the tile behind the first
+        K[0, at, 0] = 5.46875 * d ** 0.5 / 8  # (bf16 rounds the weight for d 128, for both sides alike)
+        V[0, at] = V[0, at].sign() * 2.0 ** power
+    O, lse = dsa.packed_prefill(Q, K, V, ints([0, T]), want_lse=True)
+    assert dsa.device_status() == (0, 0)
+    check(O, lse, Q, K, V, [0, T])
