@@ -53,6 +53,18 @@ def check_rows(O, lse, q, k, v, last, p_round, extra=None, what="", slack=0.0):
         assert (err <= e + 4 * FP32 * l.masked_fill(empty, 0.0).abs() + 2.0 ** -20).all(), f"{what}: lse {float(err.max())}"
 
 
+def attention64_far(q, k, v, last):
+    """(o, lse, sums of weight x |value|) like attention64, for scores of any size: differences to the row's largest are
+    taken before anything is added to them (2^60 + log 3 is 2^60 in 64 bits)."""
+    s = q @ k.mT / math.sqrt(q.shape[-1])
+    s = s.masked_fill(torch.arange(k.shape[0], device=q.device)[None] > last[:, None], -math.inf)
+    m = s.amax(-1, keepdim=True)
+    w = torch.exp(s - m)
+    total = w.sum(-1, keepdim=True)
+    w = w / total
+    return w @ v, (m + total.log())[:, 0], w @ v.abs()
+
+
 # ---- page tables, one request after the other ----------------------------------------------
 def tables_plain(lens, new, free, count, table, page, max_tokens):
     """The rules of dsa_build_tables, on lists: (slots, cu, lens, count, table, free, ok)."""

@@ -318,3 +318,23 @@ def test_large_values_under_a_maximum_that_lags(dsa, G, d, power):
     O, lse = dsa.packed_prefill(Q, K, V, ints([0, T]), want_lse=True)
     assert dsa.device_status() == (0, 0)
     check(O, lse, Q, K, V, [0, T])
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("G", [1, 2])
+@pytest.mark.parametrize("power", [10, 20, 24, 26, 28, 30, 32, 40, 60, 100])
+def test_scores_far_beyond_the_exponents_range(dsa, G, d, power):
+    """One product a score, so scores are exact: the largest of them (a few equal ones) share the row whatever their
+    size.  All that is rounded is P, O and the scores' scale, which is the same for equal scores."""
+    T = 300
+    Q, K = torch.zeros(G, T, d, dtype=torch.bfloat16, device="cuda"), torch.zeros(1, T, d, dtype=torch.bfloat16, device="cuda")
+    V = make(G, 1, T, d)[2]
+    Q[:, :, 0] = 2.0 ** power
+    K[0, :, 0] = (torch.arange(T, device="cuda") * 37 % 101 + 1).bfloat16()  # (up to 101: exact)
+    O, lse = dsa.packed_prefill(Q, K, V, ints([0, T]), want_lse=True)
+    assert dsa.device_status() == (0, 0)
+    for h in range(G):
+        o, l, a = plain.attention64_far(Q[h].double(), K[0].double(), V[0].double(), torch.arange(T, device="cuda"))
+        assert torch.isfinite(O).all()
+        assert ((O[h].double() - o).abs() <= plain.BF16 * o.abs() + 1.01 * a * (plain.BF16 + 2.0 ** -20)).all()
+        assert ((lse[h].double() - l).abs() <= 4 * plain.FP32 * l.abs() + 2.0 ** -20).all()
