@@ -821,7 +821,7 @@ k_cache_attend(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
 #pragma unroll
           for (int x = 0; x < 2; ++x) {
             top[n][x] = fmaxf(y[n][x], y[n][2 + x]);
-            grow |= top[n][x] > m[n][x] + P_LAG;
+            grow |= top[n][x] - m[n][x] > P_LAG;  // (m + P_LAG would be rounded where m is large)
           }
         }
         if (__any_sync(0xffffffffu, grow)) {
@@ -850,9 +850,11 @@ k_cache_attend(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
           float p[4];
 #pragma unroll
           for (int x = 0; x < 2; ++x) {
-            const float sh = m[n][x] == -INFINITY ? 0.f : P_OFF - m[n][x];
-            p[x] = serve_ex2(y[n][x] + sh);
-            p[2 + x] = serve_ex2(y[n][2 + x] + sh);
+            // y - m first: both are as large as the scores, so P_OFF - m would be off by half a step of m, which takes P
+            // out of fp16's range from 2^24 on
+            const float ref = m[n][x] == -INFINITY ? 0.f : m[n][x];
+            p[x] = serve_ex2(y[n][x] - ref + P_OFF);
+            p[2 + x] = serve_ex2(y[n][2 + x] - ref + P_OFF);
             l[n][x] = fmaf(p[x] + p[2 + x], iv, l[n][x]);
           }
           pb[n][0] = transpose8x8(f16x2(p[0], p[1]));

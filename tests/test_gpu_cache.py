@@ -599,3 +599,29 @@ def test_table_refusals(dsa):
                           (dict(out=dsa.Tables(ints([0] * 2), ints([0] * 3), ints([0] * 2), ints([0]))), "out.slots")):
         with pytest.raises(ValueError, match=match):
             dsa.build_tables(**{**a, **change})
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("G, n_q", [(4, 1), (4, 3)])
+@pytest.mark.parametrize("power", [10, 18, 20, 22, 24, 25, 26, 27, 28, 29, 30, 40, 60])
+def test_scores_far_beyond_the_exponents_range(dsa, d, G, n_q, power):
+    """One product a score, so scores are exact: the largest of them (equal ones) share the row whatever their size.
+    Weights are 0 or alike, so all that is rounded is O and the scores' scale, the same for equal scores."""
+    page, n = 16, 300
+    cache = dsa.PageCache.empty(20, 1, page, d)
+    at = torch.arange(20 * page, device="cuda")
+    cache.K.zero_()
+    cache.K[:, 0, :, 0] = (at * 7 % 13 + 1).float().view(20, page).to(E4M3)  # (up to 13: exact)
+    cache.V.copy_((torch.randn(20, 1, page, d, generator=gen(4), device="cuda") * 60).to(E4M3))
+    cache.k_scale.fill_(1.0)
+    cache.v_scale.fill_(1.0)
+    Q = torch.zeros(G, n_q, d, dtype=torch.bfloat16, device="cuda")
+    Q[:, :, 0] = 2.0 ** power
+    O, lse = dsa.cache_attention(Q, cache, ints([list(range(20))]), ints([n]), n_q=n_q, want_lse=True)
+    assert dsa.device_status() == (0, 0)
+    k, v = (x.double().view(20 * page, d)[:n] for x in (cache.K, cache.V))
+    for h in range(G):
+        o, l, a = plain.attention64_far(Q[h].double(), k, v, torch.arange(n - n_q, n, device="cuda"))
+        assert torch.isfinite(O).all()
+        assert ((O[h].double() - o).abs() <= plain.BF16 * o.abs() + 1.01 * a * (plain.FP16 + 2.0 ** -20)).all()
+        assert ((lse[h].double() - l).abs() <= 4 * plain.FP32 * l.abs() + 2.0 ** -20).all()
