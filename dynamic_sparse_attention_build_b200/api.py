@@ -4,6 +4,8 @@ Tensors are bf16 CUDA tensors shaped [heads, tokens, d] (any strides with a
 contiguous last dimension; a [tokens, heads, d] tensor viewed with
 ``.transpose(0, 1)`` works too).  Device memory for indices, workspace and
 outputs is allocated here with torch; the library itself allocates nothing.
+Every call runs on the tensors' device, on ``stream`` (default: the current
+stream of that device).
 """
 from __future__ import annotations
 
@@ -20,9 +22,13 @@ def _ptr(t):
     return ctypes.c_void_p(t.data_ptr()) if t is not None else ctypes.c_void_p(0)
 
 
-def _stream_ptr(stream):
-    s = stream if stream is not None else torch.cuda.current_stream()
-    return ctypes.c_void_p(s.cuda_stream)
+def _stream_ptr(stream, device):
+    """The handle of ``stream``, or of the current stream of ``device`` (the tensors')."""
+    if stream is None:
+        stream = torch.cuda.current_stream(device)
+    elif stream.device != device:
+        raise ValueError(f"the stream belongs to {stream.device}, the tensors to {device}")
+    return ctypes.c_void_p(stream.cuda_stream)
 
 
 def make_problem(Q, K, V=None, O=None, block=64) -> B.dsa_problem:
@@ -166,8 +172,9 @@ def build_indices(Q, K, patterns, block, bufs: IndexBuffers | None = None, strea
     pats_c = patterns if isinstance(patterns, ctypes.Array) else make_patterns(patterns)
     if bufs is None:
         bufs = alloc_indices(prob, pats_c, Q.device)
-    st = B.dsa_build_indices(prob, _ptr(Q), _ptr(K), pats_c, bufs.c, _ptr(bufs.workspace),
-                             bufs.workspace.numel(), _stream_ptr(stream))
+    with torch.cuda.device(Q.device):
+        st = B.dsa_build_indices(prob, _ptr(Q), _ptr(K), pats_c, bufs.c, _ptr(bufs.workspace),
+                                 bufs.workspace.numel(), _stream_ptr(stream, Q.device))
     B.check(st, "dsa_build_indices")
     bufs._pats = pats_c
     return bufs
@@ -180,7 +187,9 @@ def sparse_prefill(Q, K, V, idx: IndexBuffers, O=None, lse=None, want_lse=False,
     if lse is None and want_lse:
         lse = torch.empty(Q.shape[0], Q.shape[1], dtype=torch.float32, device=Q.device)
     prob = make_problem(Q, K, V, O, block=idx.block)
-    st = B.dsa_sparse_prefill(prob, _ptr(Q), _ptr(K), _ptr(V), idx.c, _ptr(O), _ptr(lse), _stream_ptr(stream))
+    with torch.cuda.device(Q.device):
+        st = B.dsa_sparse_prefill(prob, _ptr(Q), _ptr(K), _ptr(V), idx.c, _ptr(O), _ptr(lse),
+                                  _stream_ptr(stream, Q.device))
     B.check(st, "dsa_sparse_prefill")
     return O, lse
 
@@ -189,13 +198,18 @@ def count_pairs(Q, K, idx: IndexBuffers, stream=None) -> torch.Tensor:
     """Exact number of allowed (i, j) pairs per head (int64 tensor [Hq])."""
     pairs = torch.empty(Q.shape[0], dtype=torch.int64, device=Q.device)
     prob = make_problem(Q, K, block=idx.block)
-    B.check(B.dsa_count_pairs(prob, idx.c, _ptr(pairs), _stream_ptr(stream)), "dsa_count_pairs")
+    with torch.cuda.device(Q.device):
+        B.check(B.dsa_count_pairs(prob, idx.c, _ptr(pairs), _stream_ptr(stream, Q.device)), "dsa_count_pairs")
     return pairs
 
 
 def device_status(stream=None):
-    """(status, detail) of the current device; synchronises the stream."""
-    return B.dsa_get_device_status(_stream_ptr(stream))
+    """(status, detail) of work on ``stream`` (default: the current device's current
+    stream); synchronises it."""
+    if stream is None:
+        stream = torch.cuda.current_stream()
+    with torch.cuda.device(stream.device):
+        return B.dsa_get_device_status(_stream_ptr(stream, stream.device))
 
 
 def indices_from_lists(heads, N, block, device="cuda") -> IndexBuffers:

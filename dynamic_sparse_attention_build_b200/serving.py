@@ -304,7 +304,7 @@ class PagedLayer:
     tables, lengths and free pages, and the 8-bit cache of ``pages`` pages of ``page`` tokens.
     A request may hold ``width`` pages at most.  ``prefill`` takes prompts, short ones packed or
     one long one with sparse patterns, ``decode`` the tokens that follow.  Both enqueue work on
-    the current stream only and update lengths, tables and cache in place; ``decode``, and
+    the current stream of ``device`` only and update lengths, tables and cache in place; ``decode``, and
     ``prefill`` without patterns, can be captured into a CUDA graph.  Use it on one stream at a
     time.  If pages run out, no token of that call is
     stored and ``status`` says DSA_ERR_CAPACITY."""
@@ -351,6 +351,7 @@ class PagedLayer:
         return cache_attention(Q, self.cache, self.table, self.lens, n_q=Q.shape[1] // self.requests, want_lse=want_lse)
 
     def status(self):
-        """(status, detail) of the work on the current stream; synchronises it and clears the word."""
+        """(status, detail) of the work on the current stream of the layer's device; synchronises it and clears the
+        word."""
         from .api import device_status
-        return device_status()
+        return device_status(torch.cuda.current_stream(self.cache.K.device))
