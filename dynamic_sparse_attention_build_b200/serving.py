@@ -342,13 +342,21 @@ class PagedLayer:
 
     def decode(self, Q, K, V, new_lens=None, want_lse=False):
         """The next tokens: Q [Hq, requests * n_q, d] holds n_q rows for each request, K and V
-        the rows of the requests that get tokens, one after the other.  new_lens defaults to one
-        token for every request; a request that gets fewer than n_q attends with its newest n_q
-        all the same.  Returns (O, lse or None)."""
-        if Q.shape[1] % self.requests:
+        the rows of the requests that get tokens, one after the other.  new_lens (int32
+        [requests], -1 ends a request) defaults to one token for every request, so that K and V
+        hold one row each; a request that gets fewer than n_q attends with its newest n_q all the
+        same.  Where pages run out (see ``status``), the rows attend over the tokens from before.
+        Returns (O, lse or None)."""
+        n_q, behind = divmod(Q.shape[1], self.requests)
+        if behind:
             _refuse(f"Q has {Q.shape[1]} rows for {self.requests} requests")
-        self._store(K, V, self.ones if new_lens is None else new_lens)
-        return cache_attention(Q, self.cache, self.table, self.lens, n_q=Q.shape[1] // self.requests, want_lse=want_lse)
+        if new_lens is None:
+            # row b goes to request b: rows behind the last request's are padding where Q has one row each, too
+            if K.shape[1] < self.requests or (K.shape[1] > self.requests and n_q != 1):
+                _refuse(f"K has {K.shape[1]} rows; without new_lens each of {self.requests} requests gets one")
+            new_lens = self.ones
+        self._store(K, V, new_lens)
+        return cache_attention(Q, self.cache, self.table, self.lens, n_q=n_q, want_lse=want_lse)
 
     def status(self):
         """(status, detail) of the work on the current stream of the layer's device; synchronises it and clears the
