@@ -35,7 +35,7 @@ KIND_CODES = {"ashape": DSA_KIND_ASHAPE, "vs": DSA_KIND_VS, "block_topk": DSA_KI
 EXPORTS = ("dsa_workspace_size", "dsa_build_indices", "dsa_sparse_prefill", "dsa_count_pairs",
            "dsa_get_device_status", "dsa_selftest_wait_timeout", "dsa_status_string",
            "dsa_last_cuda_error", "dsa_build_indices_static", "dsa_set_wait_limit",
-           "dsa_packed_prefill", "dsa_build_tables", "dsa_cache_write", "dsa_cache_attention_workspace",
+           "dsa_packed_prefill", "dsa_build_tables", "dsa_build_prompt_tables", "dsa_cache_write", "dsa_cache_attention_workspace",
            "dsa_cache_attention")
 
 
@@ -111,6 +111,7 @@ def lib():
                                          ctypes.c_void_p]
         ptr, i32, i64 = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64
         L.dsa_build_tables.argtypes = [i32, ptr, ptr, ptr, i32, ptr, ptr, i32, i32, i32, ptr, ptr, ptr, ptr, ptr]
+        L.dsa_build_prompt_tables.argtypes = [*L.dsa_build_tables.argtypes[:-1], i32, ptr]
         L.dsa_cache_write.argtypes = [P(dsa_cache), ptr, ptr, i64, i64, i64, i64, ptr, i32, ptr]
         L.dsa_cache_attention_workspace.argtypes = [i32]
         L.dsa_cache_attention.argtypes = [P(dsa_cache), ptr, i32, i64, i64, ptr, i32, ptr, i32, i32, ptr, i64, i64, ptr,

@@ -43,6 +43,7 @@ constexpr int TAB_THREADS = 512;
 
 struct TableArgs {
   int n_req, width, shift, max_tokens, free_cap, in_place;
+  int prompts;  // 1: a request that gets tokens must hold none; 2: and gets all max_tokens
   const int32_t* lens;
   const int32_t* new_lens;
   int32_t* free_pages;
@@ -83,6 +84,7 @@ __global__ void __launch_bounds__(TAB_THREADS, 1) k_build_tables(const __grid_co
     const long long have = (o + page - 1) >> a.shift, all = (o + add + page - 1) >> a.shift;
     if (l < 0) flaw |= 1;
     if (held > a.width || all > a.width || o + add > 0x7fffffffll) flaw |= 2;
+    if (add > 0 && ((a.prompts > 0 && o > 0) || (a.prompts == 2 && add != a.max_tokens))) flaw |= 4;
     sum[0] += add;
     sum[1] += all - have;
     sum[2] += w < 0 ? held : 0;
@@ -113,7 +115,8 @@ __global__ void __launch_bounds__(TAB_THREADS, 1) k_build_tables(const __grid_co
   const int count = *a.free_count;
   const bool t_ok = total[0] <= a.max_tokens;
   const bool p_ok = count >= 0 && count + total[2] <= a.free_cap && count + total[2] - total[1] >= 0;
-  const bool ok = bad == 0 && t_ok && p_ok;
+  const bool s_ok = a.prompts != 2 || total[0] == a.max_tokens;
+  const bool ok = bad == 0 && t_ok && p_ok && s_ok;
   if (ok) {  // every sum fits 32 bits now
     for (int b = b0; b < b1; ++b) {
       const int w = a.new_lens[b], o = old[b], add = max(w, 0);
@@ -131,6 +134,7 @@ __global__ void __launch_bounds__(TAB_THREADS, 1) k_build_tables(const __grid_co
     }
   } else if (rank == 0 && tid == 0) {
     if (bad & 1) report(a.status, DSA_ERR_DEVICE, DETAIL_BAD_LEN);
+    else if ((bad & 4) || !s_ok) report(a.status, DSA_ERR_DEVICE, DETAIL_HELD);
     else report(a.status, DSA_ERR_CAPACITY, (bad & 2) ? DETAIL_CAP_TABLE : !t_ok ? DETAIL_CAP_TOKENS : DETAIL_CAP_PAGES);
   }
   __syncthreads();
@@ -1147,17 +1151,10 @@ dsa_status launch_attend(const dsa_cache& c, AttendArgs& a, cudaStream_t stream)
   return e == cudaSuccess ? DSA_OK : cuda_fail(e);
 }
 
-}  // namespace
-}  // namespace dsa
-
-using namespace dsa;
-
-extern "C" {
-
-dsa_status dsa_build_tables(int32_t n_req, const int32_t* lens, const int32_t* new_lens, int32_t* free_pages,
-                            int32_t free_cap, const int32_t* free_count, int32_t* block_table, int32_t width,
-                            int32_t page, int32_t max_tokens, int32_t* slots, int32_t* cu_seqlens, int32_t* lens_out,
-                            int32_t* free_count_out, dsa_stream stream) {
+dsa_status launch_tables(int32_t n_req, const int32_t* lens, const int32_t* new_lens, int32_t* free_pages,
+                         int32_t free_cap, const int32_t* free_count, int32_t* block_table, int32_t width,
+                         int32_t page, int32_t max_tokens, int32_t* slots, int32_t* cu_seqlens, int32_t* lens_out,
+                         int32_t* free_count_out, int prompts, dsa_stream stream) {
   if (n_req < 1 || width < 1 || free_cap < 1 || max_tokens < 0 || log2_page(page) < 0) return DSA_ERR_INVALID_ARG;
   if (n_req > MAX_REQ || max_tokens > (1 << 30)) return DSA_ERR_UNSUPPORTED;
   if (!lens || !new_lens || !free_pages || !free_count || !block_table || !cu_seqlens || !lens_out || !free_count_out ||
@@ -1171,6 +1168,7 @@ dsa_status dsa_build_tables(int32_t n_req, const int32_t* lens, const int32_t* n
   a.shift = log2_page(page);
   a.max_tokens = max_tokens;
   a.free_cap = free_cap;
+  a.prompts = prompts;
   a.lens = lens;
   a.new_lens = new_lens;
   a.free_pages = free_pages;
@@ -1199,6 +1197,30 @@ dsa_status dsa_build_tables(int32_t n_req, const int32_t* lens, const int32_t* n
                                : launch_pdl(k_build_tables, dim3(ctas), dim3(TAB_THREADS), smem, (cudaStream_t)stream, a);
   if (e == cudaSuccess) e = cudaGetLastError();
   return e == cudaSuccess ? DSA_OK : cuda_fail(e);
+}
+
+}  // namespace
+}  // namespace dsa
+
+using namespace dsa;
+
+extern "C" {
+
+dsa_status dsa_build_tables(int32_t n_req, const int32_t* lens, const int32_t* new_lens, int32_t* free_pages,
+                            int32_t free_cap, const int32_t* free_count, int32_t* block_table, int32_t width,
+                            int32_t page, int32_t max_tokens, int32_t* slots, int32_t* cu_seqlens, int32_t* lens_out,
+                            int32_t* free_count_out, dsa_stream stream) {
+  return launch_tables(n_req, lens, new_lens, free_pages, free_cap, free_count, block_table, width, page, max_tokens,
+                       slots, cu_seqlens, lens_out, free_count_out, 0, stream);
+}
+
+dsa_status dsa_build_prompt_tables(int32_t n_req, const int32_t* lens, const int32_t* new_lens, int32_t* free_pages,
+                                   int32_t free_cap, const int32_t* free_count, int32_t* block_table, int32_t width,
+                                   int32_t page, int32_t max_tokens, int32_t* slots, int32_t* cu_seqlens,
+                                   int32_t* lens_out, int32_t* free_count_out, int32_t single, dsa_stream stream) {
+  if (single != 0 && single != 1) return DSA_ERR_INVALID_ARG;
+  return launch_tables(n_req, lens, new_lens, free_pages, free_cap, free_count, block_table, width, page, max_tokens,
+                       slots, cu_seqlens, lens_out, free_count_out, 1 + single, stream);
 }
 
 dsa_status dsa_cache_write(const dsa_cache* cache, const void* K, const void* V, int64_t k_head_stride,

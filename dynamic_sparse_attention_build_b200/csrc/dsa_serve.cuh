@@ -12,6 +12,7 @@ namespace dsa {
 enum : unsigned {
   DETAIL_CAP_PAGES = 23, DETAIL_CAP_TOKENS = 24, DETAIL_CAP_TABLE = 25,
   DETAIL_BAD_SEQ = 37, DETAIL_BAD_LEN = 38, DETAIL_BAD_PAGE = 39, DETAIL_BAD_SLOT = 40, DETAIL_BAD_SCALE = 41,
+  DETAIL_HELD = 42,
 };
 
 // launch_pdl_cluster with dynamic shared memory.

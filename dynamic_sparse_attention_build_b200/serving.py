@@ -192,7 +192,10 @@ class Tables:
     free_count: torch.Tensor
 
 
-def build_tables(lens, new_lens, free_pages, free_count, block_table, page, max_tokens, out=None, stream=None):
+PROMPTS = {None: (), "packed": (0,), "single": (1,)}
+
+
+def build_tables(lens, new_lens, free_pages, free_count, block_table, page, max_tokens, out=None, prompts=None, stream=None):
     """Pages and slots for the tokens that each request gets next; returns ``Tables``.
 
     lens, new_lens: int32 [B], the tokens that each request has and gets (a negative number
@@ -200,7 +203,10 @@ def build_tables(lens, new_lens, free_pages, free_count, block_table, page, max_
     (free_pages int32 [F], free_count int32 [1]) are updated in place.  ``out`` takes the
     results (its ``lens`` and ``free_count`` may be the call's own).  If the pages, the table's
     width or ``max_tokens`` do not suffice, nothing changes, no token has a slot, and
-    ``device_status`` says DSA_ERR_CAPACITY."""
+    ``device_status`` says DSA_ERR_CAPACITY.  With ``prompts="packed"`` a request that gets tokens
+    must hold none, with ``prompts="single"`` one request gets all ``max_tokens`` besides (their
+    attention sees the new rows alone); otherwise nothing changes either, and the status is
+    DSA_ERR_DEVICE."""
     if not isinstance(lens, torch.Tensor) or lens.dim() != 1 or lens.numel() == 0:
         _refuse("lens must be an int32 tensor [requests]")
     if not lens.is_cuda:
@@ -218,6 +224,8 @@ def build_tables(lens, new_lens, free_pages, free_count, block_table, page, max_
         _refuse(f"a page has 16, 32, 64, 128 or 256 tokens, not {page}")
     if max_tokens < 0:
         _refuse("max_tokens must not be negative")
+    if prompts not in PROMPTS:
+        _refuse(f'prompts must be None, "packed" or "single", not {prompts!r}')
     if out is not None:
         _ints("out.slots", out.slots, (max_tokens,), dev)
         _ints("out.cu_seqlens", out.cu_seqlens, (n + 1,), dev)
@@ -225,15 +233,17 @@ def build_tables(lens, new_lens, free_pages, free_count, block_table, page, max_
         _ints("out.free_count", out.free_count, (1,), dev)
     if stream is not None or _current_device() != dev.index:
         with _elsewhere(dev, stream):
-            return build_tables(lens, new_lens, free_pages, free_count, block_table, page, max_tokens, out)
+            return build_tables(lens, new_lens, free_pages, free_count, block_table, page, max_tokens, out, prompts)
     st = _raw_stream(dev.index)
     if out is None:
         new = torch.empty(max_tokens + 2 * n + 2, dtype=torch.int32, device=dev)
         out = Tables(*new.split_with_sizes([max_tokens, n + 1, n, 1]))  # one allocation
-    B.check(B.lib().dsa_build_tables(
+    call = B.lib().dsa_build_tables if prompts is None else B.lib().dsa_build_prompt_tables
+    B.check(call(
         n, lens.data_ptr(), new_lens.data_ptr(), free_pages.data_ptr(), free_pages.numel(), free_count.data_ptr(),
         block_table.data_ptr(), width, page, max_tokens, out.slots.data_ptr(),
-        out.cu_seqlens.data_ptr(), out.lens.data_ptr(), out.free_count.data_ptr(), st), "dsa_build_tables")
+        out.cu_seqlens.data_ptr(), out.lens.data_ptr(), out.free_count.data_ptr(), *PROMPTS[prompts], st),
+        "dsa_build_tables")
     return out
 
 
@@ -320,21 +330,24 @@ class PagedLayer:
         self.free_count = torch.full((1,), pages, **ints)
         self.ones = torch.ones(requests, **ints)
 
-    def _store(self, K, V, new_lens):
+    def _store(self, K, V, new_lens, prompts=None):
         T, n = K.shape[1], self.requests
         new = torch.empty(T + n + 1, dtype=torch.int32, device=self.lens.device)
         out = Tables(new[:T], new[T:], self.lens, self.free_count)
-        build_tables(self.lens, new_lens, self.free_pages, self.free_count, self.table, self.page, T, out=out)
+        build_tables(self.lens, new_lens, self.free_pages, self.free_count, self.table, self.page, T, out=out,
+                     prompts=prompts)
         cache_write(K, V, out.slots, self.cache)
         return out
 
     def prefill(self, Q, K, V, new_lens, patterns=None, block=64):
-        """Prompts of requests that hold no tokens yet.  Q [Hq, T, d], K and V [Hkv, T, d] hold
+        """Prompts of requests that hold no tokens yet (each row sees the call's rows alone).  Q [Hq, T, d], K and V [Hkv, T, d] hold
         their rows one after the other (T may be larger than their sum: the rows behind the last
         are undefined in O), new_lens (int32 [requests]) says how many each gets: 0 for a request
         that gets none, -1 for one that has ended and gives its pages back.  With ``patterns``
-        (as for ``build_indices``) all T rows are one request's prompt.  Returns O."""
-        out = self._store(K, V, new_lens)
+        (as for ``build_indices``) all T rows are one request's prompt.  A request that gets tokens
+        though it holds some, or rows that are not one prompt's, are found on the GPU: nothing is
+        stored and ``status`` says DSA_ERR_DEVICE.  Returns O."""
+        out = self._store(K, V, new_lens, "packed" if patterns is None else "single")
         if patterns is None:
             return packed_prefill(Q, K, V, out.cu_seqlens)[0]
         from .api import build_indices, sparse_prefill

@@ -326,6 +326,15 @@ dsa_status dsa_build_tables(int32_t n_req, const int32_t* lens, const int32_t* n
                             int32_t page, int32_t max_tokens, int32_t* slots, int32_t* cu_seqlens,
                             int32_t* lens_out, int32_t* free_count_out, dsa_stream stream);
 
+/* dsa_build_tables for prompts whose attention sees their own rows alone: a request that
+ * gets tokens must hold none, and with `single` (0 or 1) one request gets all max_tokens
+ * rows.  Otherwise nothing is taken or given back, as above, and DSA_ERR_DEVICE (detail
+ * 42) is reported. */
+dsa_status dsa_build_prompt_tables(int32_t n_req, const int32_t* lens, const int32_t* new_lens, int32_t* free_pages,
+                                   int32_t free_cap, const int32_t* free_count, int32_t* block_table, int32_t width,
+                                   int32_t page, int32_t max_tokens, int32_t* slots, int32_t* cu_seqlens,
+                                   int32_t* lens_out, int32_t* free_count_out, int32_t single, dsa_stream stream);
+
 /* Stores n_tokens rows of K and V (device bf16, [Hkv] heads; strides in elements,
  * multiples of 8) in the cache; row t goes to slots[t] = page * page_size + place,
  * negative slots are passed over.  For each page and head the scale becomes the smallest

@@ -625,3 +625,52 @@ def test_scores_far_beyond_the_exponents_range(dsa, d, G, n_q, power):
         assert torch.isfinite(O).all()
         assert ((O[h].double() - o).abs() <= plain.BF16 * o.abs() + 1.01 * a * (plain.FP16 + 2.0 ** -20)).all()
         assert ((lse[h].double() - l).abs() <= 4 * plain.FP32 * l.abs() + 2.0 ** -20).all()
+
+
+@pytest.mark.parametrize("in_place", [False, True])
+@pytest.mark.parametrize("room", [1, 3])
+def test_tables_of_prompts_refuse_requests_that_hold_tokens(dsa, in_place, room):
+    """prompts: a request that gets tokens must hold none; "single": one request gets all of them.  Nothing changes
+    otherwise, and the status says so."""
+    from dynamic_sparse_attention_build_b200 import _binding as B
+    lens, free, table, page = [20, 0, 5], [3, 4, 6] + [-1] * room, [[0, 1, -1], [-1] * 3, [2, -1, -1]], 16
+
+    def run(new, tokens, prompts):
+        d = [ints(x) for x in (lens, new, free, [3], table)]
+        out = dsa.Tables(ints([5] * tokens), ints([5] * 4), d[0], d[3]) if in_place else None
+        got = dsa.build_tables(d[0], d[1], d[2], d[3], d[4], page, tokens, out=out, prompts=prompts)
+        return (got.slots.tolist(), got.cu_seqlens.tolist(), got.lens.tolist(), got.free_count.item(), d[4].tolist(), d[2].tolist())
+
+    for new, tokens, prompts, good in (
+            ([0, 17, 0], 17, "packed", True), ([-1, 17, 0], 20, "packed", True), ([0, 0, 0], 3, "packed", True),
+            ([1, 0, 0], 5, "packed", False), ([0, 4, 1], 5, "packed", False), ([0, 17, 0], 17, "single", True),
+            ([-1, 17, -1], 17, "single", True), ([0, 16, 0], 17, "single", False), ([0, 0, 0], 4, "single", False),
+            ([3, 0, 0], 3, "single", False), ([1, 0, 0], 5, None, True)):
+        want = plain.tables_plain(lens, new, free, 3, table, page, tokens)
+        status = (0, 0) if want[-1] else (B.DSA_ERR_CAPACITY, 23)  # (no room for the pages of those that end)
+        assert want[-1] or room == 1
+        if not good:
+            want, status = ([-1] * tokens, [0] * 4, lens, 3, table, free, False), (B.DSA_ERR_DEVICE, 42)
+        assert run(new, tokens, prompts) == tuple(want[:-1]), (new, tokens, prompts)
+        assert dsa.device_status() == status, (new, tokens, prompts)
+
+
+def test_paged_layer_refuses_a_prompt_behind_tokens(dsa):
+    """prefill attends over the new rows alone, so a request that holds tokens already is reported, and neither its
+    tokens nor the others' are stored; with patterns all rows are one request's."""
+    from dynamic_sparse_attention_build_b200 import _binding as B
+    layer = dsa.PagedLayer(4, 2, 64, 3, pages=60, page=16, width=40)
+    g = gen(22)
+    new = lambda h, t: torch.randn(h, t, 64, generator=g, device="cuda").bfloat16()  # noqa: E731
+    layer.prefill(new(4, 50), new(2, 50), new(2, 50), ints([20, 0, 30]))
+    assert layer.status() == (0, 0)
+    pats = [dict(kind="ashape", sink=16, window=64)] * 4
+    for lens, p in (([0, 9, 1], None), ([0, 10, 9], pats), ([10, 0, 0], pats), ([0, 9, 0], pats)):
+        layer.prefill(new(4, 10), new(2, 10), new(2, 10), ints(lens), patterns=p)
+        assert layer.status() == (B.DSA_ERR_DEVICE, 42)
+        assert layer.lens.tolist() == [20, 0, 30] and layer.free_count.item() == 60 - 4
+    layer.prefill(new(4, 10), new(2, 10), new(2, 10), ints([0, 10, 0]), patterns=pats)
+    assert layer.status() == (0, 0) and layer.lens.tolist() == [20, 10, 30]
+    layer.prefill(new(4, 8), new(2, 8), new(2, 8), ints([-1, 0, -1]))
+    layer.prefill(new(4, 8), new(2, 8), new(2, 8), ints([3, 0, 5]))
+    assert layer.status() == (0, 0) and layer.lens.tolist() == [3, 10, 5]

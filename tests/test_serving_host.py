@@ -155,3 +155,13 @@ def test_plain_attention_follows_differences():
         assert abs((float(plain.attention64(q, k2, v, last)[1]) - float(lse)) / ds - float(w[0, j])) < 1e-5
     assert float(w[0, 4]) == 0 and abs(float(w.sum()) - 1) < 1e-12
     assert torch.allclose(o, w @ v)
+
+
+@pytest.mark.parametrize("change, want", [
+    (dict(n=0), 1), (dict(width=0), 1), (dict(tokens=-1), 1), (dict(page=48), 1), (dict(lens=None), 1), (dict(n=4097), 2),
+    (dict(single=2), 1), (dict(single=-1), 1),
+])
+def test_build_prompt_tables_refuses(B, change, want):
+    a = dict(n=3, lens=A, new=A, free=A, cap=9, count=A, table=A, width=4, page=64, tokens=10, slots=A, cu=A, out=A, left=A, single=0)
+    a.update(change)
+    assert B.lib().dsa_build_prompt_tables(*a.values(), None) == want
