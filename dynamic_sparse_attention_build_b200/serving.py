@@ -65,6 +65,17 @@ def _strides(t):
     return (t.stride(0) if h > 1 else n * ts), ts
 
 
+def _rows(name, t, packed):
+    """What the library asks of a tensor's rows: 16-byte pieces, and (packed) rows and heads apart."""
+    if t.data_ptr() % 16:
+        _refuse(f"{name} must begin at a multiple of 16 bytes")
+    hs, ts = _strides(t)
+    if hs % 8 or ts % 8:
+        _refuse(f"{name}: strides must be a multiple of 8 elements")
+    if packed and t.shape[1] > 0 and (ts < t.shape[2] or hs == 0):
+        _refuse(f"{name}: rows must not overlap")
+
+
 def _ints(name, t, shape, device):
     if not isinstance(t, torch.Tensor) or t.dtype is not torch.int32:
         _refuse(f"{name} must be an int32 tensor")
@@ -320,6 +331,14 @@ class PagedLayer:
     stored and ``status`` says DSA_ERR_CAPACITY."""
 
     def __init__(self, Hq, Hkv, d, requests, pages, page=64, width=None, device="cuda"):
+        # what a call would refuse behind the one that takes pages
+        if Hq < 1 or Hkv < 1 or Hq % Hkv or Hq > 4096:
+            _refuse(f"{Hq} query heads (4096 at most) do not divide into {Hkv} KV heads")
+        if not 1 <= requests <= 4096:
+            _refuse(f"1 to 4096 requests at a time, not {requests}")
+        most = (width or pages) * page
+        if most > 0x7fffff00 or (most // 64 + 5) * requests > 0x7fffffff or pages * page > 0x7fffffff:
+            _refuse(f"{requests} requests of a width of {width or pages} pages are too many; give a smaller width")
         self.cache = PageCache.empty(pages, Hkv, page, d, device)
         dev = self.cache.K.device
         ints = dict(dtype=torch.int32, device=dev)
@@ -329,6 +348,15 @@ class PagedLayer:
         self.free_pages = torch.arange(pages, **ints)
         self.free_count = torch.full((1,), pages, **ints)
         self.ones = torch.ones(requests, **ints)
+
+    def _check(self, Q, K, V, packed):
+        """Refuses what a call behind build_tables would: by then tables and lengths have changed."""
+        c, dev = self.cache.c, self.cache.K.device
+        _tokens("Q", Q, self.Hq, None, c.d, dev)
+        _tokens("K", K, c.Hkv, Q.shape[1] if packed else None, c.d, dev)
+        _tokens("V", V, c.Hkv, K.shape[1], c.d, dev)
+        for name, t in (("Q", Q), ("K", K), ("V", V)):
+            _rows(name, t, packed)
 
     def _store(self, K, V, new_lens, prompts=None):
         T, n = K.shape[1], self.requests
@@ -347,11 +375,17 @@ class PagedLayer:
         (as for ``build_indices``) all T rows are one request's prompt.  A request that gets tokens
         though it holds some, or rows that are not one prompt's, are found on the GPU: nothing is
         stored and ``status`` says DSA_ERR_DEVICE.  Returns O."""
-        out = self._store(K, V, new_lens, "packed" if patterns is None else "single")
+        self._check(Q, K, V, True)
+        if not (0 if patterns is None else 1) <= Q.shape[1] <= 1 << 21:
+            _refuse(f"a prefill takes up to {1 << 21} rows, not {Q.shape[1]}")
         if patterns is None:
+            out = self._store(K, V, new_lens, "packed")
             return packed_prefill(Q, K, V, out.cu_seqlens)[0]
         from .api import build_indices, sparse_prefill
-        return sparse_prefill(Q, K, V, build_indices(Q, K, patterns, block))[0]
+        _ints("new_lens", new_lens, (self.requests,), self.lens.device)
+        O = sparse_prefill(Q, K, V, build_indices(Q, K, patterns, block))[0]  # first: it may refuse the patterns
+        self._store(K, V, new_lens, "single")
+        return O
 
     def decode(self, Q, K, V, new_lens=None, want_lse=False):
         """The next tokens: Q [Hq, requests * n_q, d] holds n_q rows for each request, K and V
@@ -360,8 +394,9 @@ class PagedLayer:
         hold one row each; a request that gets fewer than n_q attends with its newest n_q all the
         same.  Where pages run out (see ``status``), the rows attend over the tokens from before.
         Returns (O, lse or None)."""
+        self._check(Q, K, V, False)
         n_q, behind = divmod(Q.shape[1], self.requests)
-        if behind:
+        if behind or not 1 <= n_q <= 4096:
             _refuse(f"Q has {Q.shape[1]} rows for {self.requests} requests")
         if new_lens is None:
             # row b goes to request b: rows behind the last request's are padding where Q has one row each, too

@@ -101,7 +101,9 @@ def test_paged_layer_stays_on_its_device(cuda, args, monkeypatch):
     layer = dsa.PagedLayer.__new__(dsa.PagedLayer)
     layer.cache = types.SimpleNamespace(K=Tensor(1, 1, 1))
     layer.lens, layer.requests, layer.page = Tensor(1, 1, 4), 4, 16
-    monkeypatch.setattr(layer, "_store", lambda *a, **k: None)
+    for name in ("_store", "_check"):
+        monkeypatch.setattr(layer, name, lambda *a, **k: None)
+    monkeypatch.setattr(serving, "_ints", lambda *a: None)
     monkeypatch.setattr(api, "alloc_indices", lambda *a, **k: idx)
     monkeypatch.setattr(torch, "empty_like", lambda t, **k: O)
     layer.prefill(Q, K, V, None, patterns=[dict(kind="ashape", sink=1, window=4)] * 4)

@@ -674,3 +674,49 @@ def test_paged_layer_refuses_a_prompt_behind_tokens(dsa):
     layer.prefill(new(4, 8), new(2, 8), new(2, 8), ints([-1, 0, -1]))
     layer.prefill(new(4, 8), new(2, 8), new(2, 8), ints([3, 0, 5]))
     assert layer.status() == (0, 0) and layer.lens.tolist() == [3, 10, 5]
+
+
+@pytest.mark.parametrize("call", ["prefill", "sparse", "decode"])
+@pytest.mark.parametrize("name, how, match", [
+    ("Q", "float", "bfloat16"), ("Q", "heads", "dimension 0"), ("Q", "d", "dimension 2"), ("K", "float", "bfloat16"),
+    ("K", "heads", "dimension 0"), ("V", "rows", "dimension 1"), ("V", "host", "CUDA"), ("Q", "shifted", "16 bytes"),
+    ("K", "shifted", "16 bytes"), ("V", "odd", "multiple of 8"), ("new_lens", "long", "int32"), ("new_lens", "short", "shape"),
+    ("Q", "none", " has "), ("patterns", "kind", None),
+])
+def test_paged_layer_refuses_before_it_changes_anything(dsa, call, name, how, match):
+    layer = dsa.PagedLayer(4, 2, 64, 3, pages=60, page=16, width=40)
+    g = gen(23)
+    new = lambda h, t: torch.randn(h, t, 64, generator=g, device="cuda").bfloat16()  # noqa: E731
+    layer.prefill(new(4, 50), new(2, 50), new(2, 50), ints([20, 0, 30]))
+    rows = 3 if call == "decode" else 40
+    a = dict(Q=new(4, rows), K=new(2, rows), V=new(2, rows), new_lens=ints([1, 1, 1] if call == "decode" else [0, rows, 0]))
+    if call == "sparse":
+        a["patterns"] = [dict(kind="ashape", sink=16, window=64)] * 4
+    if name == "patterns":
+        if call != "sparse":
+            pytest.skip("patterns are the sparse prefill's")
+        a["patterns"] = [dict(kind="ashape", sink=-1, window=64)] * 4
+    else:
+        t = a[name]
+        wide = torch.zeros(*t.shape[:-1], 72, dtype=torch.bfloat16, device="cuda") if name != "new_lens" else None
+        a[name] = {"float": lambda: t.float(), "heads": lambda: t[:1], "d": lambda: torch.cat([t, t], 2), "rows": lambda: t[:, :2],
+                   "host": lambda: t.cpu(), "shifted": lambda: wide[:, :, 1:65], "odd": lambda: torch.zeros(2, rows, 68, dtype=torch.bfloat16, device="cuda")[:, :, :64],
+                   "long": lambda: t.long(), "short": lambda: t[:2], "none": lambda: t[:, :0]}[how]()
+    held = [x.clone() for x in (layer.lens, layer.table, layer.free_pages, layer.free_count, layer.cache.K.view(torch.uint8),
+                                layer.cache.V.view(torch.uint8), layer.cache.k_scale, layer.cache.v_scale)]
+    with pytest.raises(Exception) as e:
+        (layer.decode if call == "decode" else layer.prefill)(**a)
+    if match:
+        assert e.type is ValueError and match in str(e.value)
+    assert layer.status() == (0, 0)
+    for x, y in zip(held, (layer.lens, layer.table, layer.free_pages, layer.free_count, layer.cache.K.view(torch.uint8),
+                           layer.cache.V.view(torch.uint8), layer.cache.k_scale, layer.cache.v_scale)):
+        assert torch.equal(x, y)
+
+
+def test_paged_layer_refuses_sizes(dsa):
+    for change, match in ((dict(Hq=3), "divide"), (dict(requests=0), "requests"), (dict(requests=4097), "requests"),
+                          (dict(Hq=8192, Hkv=8192), "heads"), (dict(width=1 << 27), "width")):
+        a = dict(Hq=4, Hkv=2, d=64, requests=3, pages=4, page=16)
+        with pytest.raises(ValueError, match=match):
+            dsa.PagedLayer(**{**a, **change})
