@@ -165,3 +165,19 @@ def test_build_prompt_tables_refuses(B, change, want):
     a = dict(n=3, lens=A, new=A, free=A, cap=9, count=A, table=A, width=4, page=64, tokens=10, slots=A, cu=A, out=A, left=A, single=0)
     a.update(change)
     assert B.lib().dsa_build_prompt_tables(*a.values(), None) == want
+
+
+def test_import_needs_no_private_names_of_torch():
+    """Importing loads nothing: what a torch without CUDA lacks is looked up by the first call."""
+    import subprocess
+    import sys
+    code = ("import torch\n"
+            "for n in ('_cuda_getCurrentRawStream', '_cuda_getDevice'):\n"
+            "    if hasattr(torch._C, n): delattr(torch._C, n)\n"
+            "import dynamic_sparse_attention_build_b200 as dsa\n"
+            "t, i = torch.zeros(2, 5, 64, dtype=torch.bfloat16), torch.zeros(3, dtype=torch.int32)\n"
+            "try:\n    dsa.packed_prefill(t, t, t, i)\n"
+            "except ValueError as e:\n    print('refused:', e)\n")
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True)
+    assert r.returncode == 0 and "CUDA" in r.stdout, r.stderr
