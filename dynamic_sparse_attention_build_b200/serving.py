@@ -23,9 +23,9 @@ def _refuse(what):
 
 
 # The handle of a device's current stream, and the current device: 0.1 us each, where
-# torch.cuda.current_stream takes 3 us.  A torch without CUDA lacks them; no call gets that far there.
-_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-_current_device = getattr(torch._C, "_cuda_getDevice", None)
+# torch.cuda.current_stream takes 3 us.  A torch may lack them (one without CUDA does).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", lambda device: torch.cuda.current_stream(device).cuda_stream)
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
 @contextlib.contextmanager
