@@ -1104,7 +1104,8 @@ dsa_status validate_cache(const dsa_cache* c) {
   if (c->Hkv > 4096 || (int64_t)c->num_pages * c->page > 0x7fffffffll) return DSA_ERR_UNSUPPORTED;
   if (!c->K || !c->V || !c->k_scale || !c->v_scale || !serve_aligned16(c->K) || !serve_aligned16(c->V)) return DSA_ERR_INVALID_ARG;
   if (c->token_stride < c->d || c->token_stride % 16 || c->head_stride % 16 || c->page_stride % 16) return DSA_ERR_INVALID_ARG;
-  if ((c->Hkv > 1 && c->head_stride < c->d) || (c->num_pages > 1 && c->page_stride < c->d)) return DSA_ERR_INVALID_ARG;
+  ServeDim dims[3] = {{c->page, c->token_stride}, {c->Hkv, c->head_stride}, {c->num_pages, c->page_stride}};
+  if (!serve_apart(c->d, dims)) return DSA_ERR_INVALID_ARG;  // pages would overwrite each other
   return DSA_OK;
 }
 
@@ -1232,6 +1233,19 @@ dsa_status dsa_cache_write(const dsa_cache* cache, const void* K, const void* V,
   if (n_tokens == 0) return DSA_OK;
   if (!K || !V || !slots || !serve_aligned16(K) || !serve_aligned16(V)) return DSA_ERR_INVALID_ARG;
   if (k_token_stride % 8 || v_token_stride % 8 || k_head_stride % 8 || v_head_stride % 8) return DSA_ERR_INVALID_ARG;
+  // keys and values that overlap (which reading them bears), and their scales
+  auto distance = [](const void* x, const void* y) {
+    const uintptr_t a = reinterpret_cast<uintptr_t>(x), b = reinterpret_cast<uintptr_t>(y);
+    return (int64_t)(a < b ? b - a : a - b);
+  };
+  ServeDim dims[4] = {{cache->page, cache->token_stride},
+                      {cache->Hkv, cache->head_stride},
+                      {cache->num_pages, cache->page_stride},
+                      {2, distance(cache->K, cache->V)}};
+  if (!serve_apart(cache->d, dims) ||
+      distance(cache->k_scale, cache->v_scale) < (int64_t)cache->num_pages * cache->Hkv * (int64_t)sizeof(float))
+    return DSA_ERR_INVALID_ARG;
+  if (n_tokens > (1 << 30)) return DSA_ERR_UNSUPPORTED;
   unsigned* st = status_ptr((cudaStream_t)stream);
   if (st == nullptr) return cuda_fail(cudaGetLastError());
   StoreArgs a;
@@ -1285,7 +1299,8 @@ dsa_status dsa_cache_attention(const dsa_cache* cache, const void* Q, int32_t Hq
   if (!Q || !O || !block_table || !lens || !workspace) return DSA_ERR_INVALID_ARG;
   if (!serve_aligned16(Q) || !serve_aligned16(O) || !serve_aligned16(workspace)) return DSA_ERR_INVALID_ARG;
   if (q_head_stride % 8 || q_token_stride % 8 || o_head_stride % 8 || o_token_stride % 8) return DSA_ERR_INVALID_ARG;
-  if (o_token_stride < cache->d || (Hq > 1 && o_head_stride < cache->d)) return DSA_ERR_INVALID_ARG;  // rows of O overlap
+  ServeDim o_dims[2] = {{(int64_t)n_req * n_q, o_token_stride}, {Hq, o_head_stride}};
+  if (o_token_stride < cache->d || !serve_apart(cache->d, o_dims)) return DSA_ERR_INVALID_ARG;  // rows of O overlap
   if ((int64_t)n_req * cache->Hkv * ceil_div(n_q * (Hq / cache->Hkv), 16) > 0x7fffffffll) return DSA_ERR_UNSUPPORTED;
   if (workspace_bytes < (size_t)dsa_cache_attention_workspace(cache->d)) return DSA_ERR_CAPACITY;
   unsigned* st = status_ptr((cudaStream_t)stream);

@@ -705,6 +705,8 @@ extern "C" dsa_status dsa_packed_prefill(const dsa_problem* p, const void* Q, co
   if ((p->Hq > 1 && (p->q_head_stride == 0 || p->o_head_stride == 0)) ||
       (p->Hkv > 1 && (p->k_head_stride == 0 || p->v_head_stride == 0)))
     return DSA_ERR_INVALID_ARG;
+  ServeDim o_dims[2] = {{p->N, p->o_token_stride}, {p->Hq, p->o_head_stride}};
+  if (!serve_apart(p->d, o_dims)) return DSA_ERR_INVALID_ARG;  // rows of O overlap
   if (n_seq < 0 || (n_seq > 0 && cu_seqlens == nullptr)) return DSA_ERR_INVALID_ARG;
   if (!Q || !K || !V || !O) return DSA_ERR_INVALID_ARG;
   if (!serve_aligned16(Q) || !serve_aligned16(K) || !serve_aligned16(V) || !serve_aligned16(O)) return DSA_ERR_INVALID_ARG;

@@ -2,6 +2,7 @@
 #pragma once
 
 #include <atomic>
+#include <utility>
 
 #include "dsa_common.cuh"
 #include "dsa_internal.h"
@@ -59,6 +60,25 @@ inline cudaError_t serve_allow_smem(int dev, int bytes) {
   const cudaError_t e = cudaFuncSetAttribute(Kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
   if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
   return e;
+}
+
+// A dimension of a strided array: its size, and the distance of its neighbours.
+struct ServeDim {
+  int64_t n, stride;
+};
+// Whether the array's rows of `row` units are apart: with the dimensions in order of their strides, each steps over all
+// that the smaller ones span.  (Layouts that interleave rows in any other way are taken for overlapping ones.)
+template <int N>
+inline bool serve_apart(int64_t row, ServeDim (&dims)[N]) {
+  for (int i = 1; i < N; ++i)
+    for (int j = i; j > 0 && dims[j].stride < dims[j - 1].stride; --j) std::swap(dims[j], dims[j - 1]);
+  __int128 span = row;
+  for (const ServeDim& d : dims) {
+    if (d.n < 2) continue;
+    if (d.stride < span) return false;
+    span += (__int128)(d.n - 1) * d.stride;
+  }
+  return true;
 }
 
 inline bool serve_aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }

@@ -65,6 +65,24 @@ def _strides(t):
     return (t.stride(0) if h > 1 else n * ts), ts
 
 
+def _apart(row, dims):
+    """Whether rows of `row` elements are apart: dims are (size, stride), and with them in order of
+    their strides each steps over all that the smaller ones span."""
+    span = row
+    for n, stride in sorted(dims, key=lambda x: x[1]):
+        if n > 1:
+            if stride < span:
+                return False
+            span += (n - 1) * stride
+    return True
+
+
+def _output(O, heads, tokens, d, device):
+    _tokens("O", O, heads, tokens, d, device)
+    if O.numel() and not _apart(d, ((heads, O.stride(0)), (tokens, O.stride(1)))):
+        _refuse("O: rows must not overlap")
+
+
 def _rows(name, t, packed):
     """What the library asks of a tensor's rows: 16-byte pieces, and (packed) rows and heads apart."""
     if t.data_ptr() % 16:
@@ -121,7 +139,7 @@ def packed_prefill(Q, K, V, cu_seqlens, O=None, lse=None, want_lse=False, stream
         _refuse("cu_seqlens must be an int32 tensor [sequences + 1]")
     _ints("cu_seqlens", cu_seqlens, cu_seqlens.shape, dev)
     if O is not None:
-        _tokens("O", O, Hq, T, d, dev)
+        _output(O, Hq, T, d, dev)
     if stream is not None or _current_device() != dev.index:
         with _elsewhere(dev, stream):
             return packed_prefill(Q, K, V, cu_seqlens, O, lse, want_lse)
@@ -180,7 +198,7 @@ class PageCache:
         token = K.stride(2)
         head = K.stride(1) if Hkv > 1 else page * token
         whole = K.stride(0) if pages > 1 else Hkv * page * token
-        if token < d or head < d or whole < d:
+        if token < d or not _apart(d, ((page, token), (Hkv, head), (pages, whole))):
             _refuse("pages, heads and tokens of the cache must not overlap")
         object.__setattr__(self, "c", B.dsa_cache(pages, Hkv, page, d, whole, head, token, K.data_ptr(), V.data_ptr(),
                                                   self.k_scale.data_ptr(), self.v_scale.data_ptr()))
@@ -298,7 +316,7 @@ def cache_attention(Q, cache, block_table, lens, n_q=1, O=None, lse=None, want_l
     if n_q < 1 or T != n * n_q:
         _refuse(f"Q has {T} rows, not {n_q} for each of {n} requests")
     if O is not None:
-        _tokens("O", O, Hq, T, d, dev)
+        _output(O, Hq, T, d, dev)
     need = B.lib().dsa_cache_attention_workspace(d)
     if workspace is not None:
         if workspace.device != dev or not workspace.is_contiguous() or workspace.nbytes < need:

@@ -279,7 +279,7 @@ dsa_status dsa_set_wait_limit(uint64_t limit_ns);
  * O: device bf16 with the problem's o strides; lse: optional device float [Hq * N].
  * Rows of no sequence (behind the last, say) are left as they were.  A sequence whose
  * bounds are malformed is skipped and reported as DSA_ERR_DEVICE.  A head stride of 0
- * is DSA_ERR_INVALID_ARG unless there is one head. */
+ * is DSA_ERR_INVALID_ARG unless there is one head, and so are rows of O that overlap. */
 dsa_status dsa_packed_prefill(const dsa_problem* p, const void* Q, const void* K, const void* V,
                               const int32_t* cu_seqlens, int32_t n_seq, void* O, float* lse,
                               dsa_stream stream);
@@ -290,7 +290,9 @@ dsa_status dsa_packed_prefill(const dsa_problem* p, const void* Q, const void* K
  * d in {64, 128}: value x of token t of a page and head is at
  *   page * page_stride + head * head_stride + t * token_stride + x   (bytes, multiples
  * of 16; base pointers 16-byte aligned), and stands for itself times the page's scale
- * k_scale / v_scale [num_pages * Hkv], a float in 2^-64 .. 2^64.  dsa_cache_write
+ * k_scale / v_scale [num_pages * Hkv], a float in 2^-64 .. 2^64.  The rows of d bytes
+ * must not overlap: with the dimensions in the order of their strides, each steps over all
+ * that the smaller ones span.  dsa_cache_write
  * writes powers of two in 2^-60 .. 2^60.  A page's scales need a valid value (2^-60,
  * say) before tokens are first written behind its beginning.
  */
@@ -345,7 +347,8 @@ dsa_status dsa_build_prompt_tables(int32_t n_req, const int32_t* lens, const int
  * The rows of one page follow each other, in the call as in the page (slots as
  * dsa_build_tables makes them); rows of a page behind the last new one count as empty.  A
  * page named in two places of one call ends with undefined contents.  A slot beyond the
- * cache, or a scale outside its range that has to be kept, is reported as DSA_ERR_DEVICE. */
+ * cache, or a scale outside its range that has to be kept, is reported as DSA_ERR_DEVICE.
+ * K and V of the cache, and their scales, must not overlap here.  At most 2^30 rows. */
 dsa_status dsa_cache_write(const dsa_cache* cache, const void* K, const void* V, int64_t k_head_stride,
                            int64_t k_token_stride, int64_t v_head_stride, int64_t v_token_stride,
                            const int32_t* slots, int32_t n_tokens, dsa_stream stream);

@@ -181,3 +181,50 @@ def test_import_needs_no_private_names_of_torch():
     root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
     r = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True)
     assert r.returncode == 0 and "CUDA" in r.stdout, r.stderr
+
+
+# (page, head and token stride) of 9 pages of 64 tokens, 2 heads, d 128
+@pytest.mark.parametrize("strides, good", [
+    ((2 * 64 * 128, 64 * 128, 128), True), ((2 * 64 * 128, 128, 2 * 128), True),  # [pages, heads, page, d], [pages, page, heads, d]
+    ((64 * 128, 9 * 64 * 128, 128), True), ((128, 9 * 64 * 128, 9 * 128), True),  # heads in front; pages inside
+    ((3 * 64 * 144, 64 * 144, 144), True),                                           # gaps everywhere
+    ((64 * 128, 64 * 128, 128), False), ((2 * 64 * 128 - 16, 64 * 128, 128), False), ((2 * 64 * 128, 64 * 128 - 16, 128), False),
+    ((2 * 64 * 128, 128, 128), False), ((2 * 64 * 128, 144, 2 * 128), False), ((128, 128, 128), False),
+])
+def test_caches_whose_pages_overlap_are_refused(B, strides, good):
+    c = cache(B, page_stride=strides[0], head_stride=strides[1], token_stride=strides[2], V=1 << 30, v_scale=1 << 29)
+    want = B.DSA_OK if good else B.DSA_ERR_INVALID_ARG
+    assert B.lib().dsa_cache_write(ctypes.byref(c), None, None, 0, 0, 0, 0, None, 0, None) == want
+    assert B.lib().dsa_cache_attention(ctypes.byref(c), A, 4, 512, 128, A, 3, A, 0, 1, A, 512, 128, None, A, 1 << 30, None) == want
+
+
+@pytest.mark.parametrize("change, good", [
+    (dict(V=A), False), (dict(V=A + 64 * 128), False), (dict(V=A - 128), False), (dict(V=A + 9 * 2 * 64 * 128), True),
+    (dict(V=A - 9 * 2 * 64 * 128), True), (dict(page_stride=4 * 64 * 128, V=A + 2 * 64 * 128), True),  # K and V of one array
+    (dict(token_stride=256, head_stride=64 * 256, page_stride=2 * 64 * 256, V=A + 128), True),
+    (dict(k_scale=A, v_scale=A), False), (dict(k_scale=A, v_scale=A + 4 * 9 * 2 - 4), False), (dict(k_scale=A, v_scale=A + 4 * 9 * 2), True),
+])
+def test_a_store_into_keys_and_values_that_overlap_is_refused(B, change, good):
+    """Reading them is fine: keys may be the values."""
+    c = cache(B, **{**dict(V=1 << 30, v_scale=1 << 29), **change})
+    # a call that passes these checks is refused for its number of tokens
+    got = B.lib().dsa_cache_write(ctypes.byref(c), A, A, 512, 128, 512, 128, A, (1 << 30) + 1, None)
+    assert got == (B.DSA_ERR_UNSUPPORTED if good else B.DSA_ERR_INVALID_ARG)
+    assert B.lib().dsa_cache_attention(ctypes.byref(c), A, 4, 512, 128, A, 3, A, 0, 1, A, 512, 128, None, A, 1 << 30, None) == B.DSA_OK
+
+
+@pytest.mark.parametrize("oh, ot, good", [(512, 128, True), (128, 512, True), (128, 128, False), (256, 192, False), (200, 400, False)])
+def test_outputs_whose_rows_overlap_are_refused(B, oh, ot, good):
+    """O of 4 heads and 4 rows, d 128.  (Good strides are refused for the missing workspace or the odd length instead.)"""
+    got = B.lib().dsa_cache_attention(ctypes.byref(cache(B)), A, 4, 512, 128, A, 3, A, 4, 1, A, oh, ot, None, A, 10, None)
+    assert got == (B.DSA_ERR_CAPACITY if good else B.DSA_ERR_INVALID_ARG)
+    p = problem(B, N=4, o_head_stride=oh, o_token_stride=ot)
+    assert B.lib().dsa_packed_prefill(ctypes.byref(p), A, A, A, A, 0, A, None, None) == (B.DSA_OK if good else B.DSA_ERR_INVALID_ARG)
+
+
+def test_cache_layouts_whose_pages_overlap_are_refused_in_python(B, monkeypatch):
+    from dynamic_sparse_attention_build_b200 import serving
+    assert serving._apart(64, ((9, 8192), (2, 4096), (16, 256))) and serving._apart(64, ((1, 0), (2, 64), (1, 5)))
+    assert serving._apart(64, ((9, 64), (2, 64 * 9 * 16), (16, 64 * 9)))
+    for bad in (((9, 4096), (2, 4096), (16, 256)), ((9, 8192), (2, 64), (16, 64)), ((9, 0), (2, 64), (16, 128)), ((2, 32),)):
+        assert not serving._apart(64, bad)
