@@ -3,8 +3,10 @@ over packed prompts, the page tables of a paged cache, the store of keys and val
 and the attention of new tokens over that cache.
 
 Token tensors are bf16 CUDA tensors shaped [heads, tokens, d] as in ``api``.  Arguments are
-checked here before the library sees a pointer: a wrong shape, type, device or layout raises
-``ValueError`` and enqueues nothing.  Every call runs on ``stream`` (default: the current
+checked here before the library sees a pointer: a wrong shape, type, device or a last dimension
+that is not contiguous raises ``ValueError`` and enqueues nothing.  What the library itself asks
+of pointers, strides and sizes (rows on 16-byte boundaries, say) raises ``DSAError`` and enqueues
+nothing either.  Every call runs on ``stream`` (default: the current
 stream of the tensors' device); what it allocates belongs to that stream.
 """
 from __future__ import annotations
@@ -114,9 +116,16 @@ def _table(t):
 def _lse(lse, want, shape, device):
     if lse is None:
         return torch.empty(shape, dtype=torch.float32, device=device) if want else None
-    if lse.dtype is not torch.float32 or lse.device != device or lse.shape != shape or not lse.is_contiguous():
+    if not isinstance(lse, torch.Tensor) or lse.dtype is not torch.float32 or lse.device != device or lse.shape != shape or not lse.is_contiguous():
         _refuse(f"lse must be a contiguous float32 tensor {tuple(shape)} on {device}")
     return lse
+
+
+def _workspace(workspace, need, device):
+    if workspace is not None:
+        if (not isinstance(workspace, torch.Tensor) or workspace.device != device or not workspace.is_contiguous()
+                or workspace.nbytes < need or workspace.data_ptr() % 16):
+            _refuse(f"workspace must hold {need} bytes on {device}, from a multiple of 16 bytes on")
 
 
 def packed_prefill(Q, K, V, cu_seqlens, O=None, lse=None, want_lse=False, stream=None):
@@ -318,9 +327,7 @@ def cache_attention(Q, cache, block_table, lens, n_q=1, O=None, lse=None, want_l
     if O is not None:
         _output(O, Hq, T, d, dev)
     need = B.lib().dsa_cache_attention_workspace(d)
-    if workspace is not None:
-        if workspace.device != dev or not workspace.is_contiguous() or workspace.nbytes < need:
-            _refuse(f"workspace must hold {need} bytes on {dev}")
+    _workspace(workspace, need, dev)
     if stream is not None or _current_device() != dev.index:
         with _elsewhere(dev, stream):
             return cache_attention(Q, cache, block_table, lens, n_q, O, lse, want_lse, workspace)

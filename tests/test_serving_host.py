@@ -228,3 +228,18 @@ def test_cache_layouts_whose_pages_overlap_are_refused_in_python(B, monkeypatch)
     assert serving._apart(64, ((9, 64), (2, 64 * 9 * 16), (16, 64 * 9)))
     for bad in (((9, 4096), (2, 4096), (16, 256)), ((9, 8192), (2, 64), (16, 64)), ((9, 0), (2, 64), (16, 128)), ((2, 32),)):
         assert not serving._apart(64, bad)
+
+
+def test_lse_and_workspace_that_are_no_tensors_are_refused():
+    from dynamic_sparse_attention_build_b200 import serving
+    dev = torch.device("cpu")
+    for bad in ([0.0] * 4, 7, torch.zeros(2, 3), torch.zeros(2, 2, dtype=torch.float64), torch.zeros(2, 4)[:, ::2]):
+        with pytest.raises(ValueError, match="lse"):
+            serving._lse(bad, False, (2, 2), dev)
+    good = torch.zeros(2, 2)
+    assert serving._lse(good, False, (2, 2), dev) is good and serving._lse(None, False, (2, 2), dev) is None
+    for bad in (1 << 20, [0] * 64, torch.zeros(15), torch.zeros(64)[::2], torch.zeros(65, dtype=torch.uint8)[1:]):
+        with pytest.raises(ValueError, match="workspace"):
+            serving._workspace(bad, 64, dev)
+    for good in (None, torch.zeros(16), torch.zeros(80, dtype=torch.uint8)):
+        serving._workspace(good, 64, dev)
