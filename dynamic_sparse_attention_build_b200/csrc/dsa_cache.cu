@@ -60,7 +60,7 @@ __global__ void __launch_bounds__(TAB_THREADS, 1) k_build_tables(const __grid_co
   pdl_prologue();
   extern __shared__ int sh[];
   const int n = a.n_req;
-  int* cu = sh;                  // [n + 1] first new token of each request
+  int* cu = sh;                  // [n + 1] first new token of each request; its length if the call is refused
   int* take = cu + n + 1;        // [n + 1] first page taken
   int* give = take + n + 1;      // [n + 1] first page given back
   int* old = give + n + 1;       // [n] tokens kept
@@ -132,10 +132,13 @@ __global__ void __launch_bounds__(TAB_THREADS, 1) k_build_tables(const __grid_co
       take[n] = (int)total[1];
       give[n] = (int)total[2];
     }
-  } else if (rank == 0 && tid == 0) {
-    if (bad & 1) report(a.status, DSA_ERR_DEVICE, DETAIL_BAD_LEN);
-    else if ((bad & 4) || !s_ok) report(a.status, DSA_ERR_DEVICE, DETAIL_HELD);
-    else report(a.status, DSA_ERR_CAPACITY, (bad & 2) ? DETAIL_CAP_TABLE : !t_ok ? DETAIL_CAP_TOKENS : DETAIL_CAP_PAGES);
+  } else {
+    for (int b = b0; b < b1; ++b) cu[b] = a.lens[b];  // they stay: kept here, where no write of this call reaches them
+    if (rank == 0 && tid == 0) {
+      if (bad & 1) report(a.status, DSA_ERR_DEVICE, DETAIL_BAD_LEN);
+      else if ((bad & 4) || !s_ok) report(a.status, DSA_ERR_DEVICE, DETAIL_HELD);
+      else report(a.status, DSA_ERR_CAPACITY, (bad & 2) ? DETAIL_CAP_TABLE : !t_ok ? DETAIL_CAP_TOKENS : DETAIL_CAP_PAGES);
+    }
   }
   __syncthreads();
   const int at = rank * TAB_THREADS + tid;
@@ -197,7 +200,7 @@ __global__ void __launch_bounds__(TAB_THREADS, 1) k_build_tables(const __grid_co
   if (a.in_place && gridDim.x > 1) cluster_sync();  // every CTA has read lengths and count
   for (int i = at; i <= n; i += nthreads) {
     a.cu[i] = ok ? cu[i] : 0;
-    if (i < n) a.lens_out[i] = ok ? old[i] + (cu[i + 1] - cu[i]) : a.lens[i];
+    if (i < n) a.lens_out[i] = ok ? old[i] + (cu[i + 1] - cu[i]) : cu[i];
   }
   if (at == 0) *a.count_out = ok ? count + freed - (int)total[1] : count;
 }

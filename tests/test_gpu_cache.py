@@ -720,3 +720,17 @@ def test_paged_layer_refuses_sizes(dsa):
         a = dict(Hq=4, Hkv=2, d=64, requests=3, pages=4, page=16)
         with pytest.raises(ValueError, match=match):
             dsa.PagedLayer(**{**a, **change})
+
+
+@pytest.mark.parametrize("n", [3, 700])
+@pytest.mark.parametrize("tokens", [0, 40, 9000])
+def test_tables_whose_lengths_overlap_in_part(dsa, n, tokens):
+    """lens_out one place behind lens in the same memory: refused as a whole, the lengths still come out right."""
+    from dynamic_sparse_attention_build_b200 import _binding as B
+    lens = [(i * 7) % 50 for i in range(n)]
+    buf = ints(lens + [0])
+    out = dsa.Tables(ints([5] * tokens), ints([5] * (n + 1)), buf[1:], ints([5]))
+    table = torch.full((n, 4), 1, dtype=torch.int32, device="cuda")
+    dsa.build_tables(buf[:n], ints([1000] * n), ints([0] * 9), ints([2]), table, 16, tokens, out=out)
+    assert dsa.device_status() == (B.DSA_ERR_CAPACITY, 25)
+    assert out.lens.tolist() == lens and out.free_count.item() == 2 and (out.slots == -1).all() and (out.cu_seqlens == 0).all()
