@@ -734,3 +734,49 @@ def test_tables_whose_lengths_overlap_in_part(dsa, n, tokens):
     dsa.build_tables(buf[:n], ints([1000] * n), ints([0] * 9), ints([2]), table, 16, tokens, out=out)
     assert dsa.device_status() == (B.DSA_ERR_CAPACITY, 25)
     assert out.lens.tolist() == lens and out.free_count.item() == 2 and (out.slots == -1).all() and (out.cu_seqlens == 0).all()
+
+
+@pytest.mark.parametrize("Hq, Hkv, d, n, n_q", [(4, 2, 128, 1500, 1), (8, 8, 64, 4096, 1), (16, 2, 128, 4096, 2), (4, 1, 64, 2000, 3)])
+def test_attention_of_many_requests(dsa, Hq, Hkv, d, n, n_q):
+    """More requests than keep the planned CTAs on an SM (their lengths lie in shared memory), a third without keys."""
+    rng = random.Random(n)
+    lens = [rng.choice([0, rng.randint(0, 5), rng.randint(0, 200)]) for _ in range(n)]
+    cache, table, dl, Q = attend_inputs(dsa, Hq, Hkv, d, 16, lens, n_q)
+    O, lse = dsa.cache_attention(Q, cache, table, dl, n_q=n_q, want_lse=True)
+    assert dsa.device_status() == (0, 0)
+    # all at once: what check_attend takes request by request, at 200 keys each
+    page, G, W = 16, Hq // Hkv, 200
+    at = torch.arange(W, device="cuda")
+    pages = table.clamp(min=0).long().gather(1, (at // page).clamp(max=table.shape[1] - 1).expand(n, W))
+    live = at[None] < dl[:, None]
+    worst = 0.0
+    for h in range(Hkv):
+        k, v = (torch.where(live[..., None], x[pages, h, at % page].double() * s[pages, h].double()[..., None], 0.0)
+                for x, s in ((cache.K, cache.k_scale), (cache.V, cache.v_scale)))
+        vs = cache.v_scale[pages, h].double()
+        for q in range(h * G, (h + 1) * G):
+            x = Q[q].view(n, n_q, d).double()
+            s = x @ k.mT / math.sqrt(d)
+            s = s.masked_fill(at > (dl[:, None] - n_q + torch.arange(n_q, device="cuda"))[..., None], -math.inf)
+            l = torch.logsumexp(s, -1)
+            empty = l == -math.inf
+            w = torch.where(s == -math.inf, 0.0, torch.exp(s - l.masked_fill(empty, 0.0)[..., None]))
+            o, a = w @ v, w @ v.abs()
+            e = (d + 8) * plain.FP32 * (x.abs() @ k.abs().amax(1)[..., None])[..., 0] / math.sqrt(d) + 2.0 ** -19
+            tol = plain.BF16 * o.abs() + 1.01 * a * (plain.FP16 + 4.2 * e[..., None] + 2.0 ** -20) + 2.0 ** -126 \
+                + W * 448.0 * 2.0 ** -35 * (w * vs[:, None]).amax(-1, keepdim=True)
+            got, got_l = O[q].view(n, n_q, d).double(), lse[q].view(n, n_q).double()
+            assert ((got - o).abs() <= tol).all() and torch.equal(got_l == -math.inf, empty)
+            err = (got_l - l).masked_fill(empty, 0.0).abs()
+            assert (err <= e + 4 * plain.FP32 * l.masked_fill(empty, 0.0).abs() + 2.0 ** -20).all()
+            worst = max(worst, float(err.max()))
+    assert (O.view(Hq, n, n_q, d)[:, (dl == 0)] == 0).all()
+
+
+@pytest.mark.parametrize("Hq, Hkv, d, lens, n_q", [(16, 2, 128, [100, 0, 299, 300, 301], 300), (1, 1, 64, [700, 3], 600),
+                                                   (4, 2, 64, [5, 1000], 129)])
+def test_attention_of_more_tokens_than_keys(dsa, Hq, Hkv, d, lens, n_q):
+    cache, table, dl, Q = attend_inputs(dsa, Hq, Hkv, d, 32, lens, n_q)
+    O, lse = dsa.cache_attention(Q, cache, table, dl, n_q=n_q, want_lse=True)
+    assert dsa.device_status() == (0, 0)
+    check_attend(O, lse, Q, cache, table, lens, n_q)

@@ -338,3 +338,15 @@ def test_scores_far_beyond_the_exponents_range(dsa, G, d, power):
         assert torch.isfinite(O).all()
         assert ((O[h].double() - o).abs() <= plain.BF16 * o.abs() + 1.01 * a * (plain.BF16 + 2.0 ** -20)).all()
         assert ((lse[h].double() - l).abs() <= 4 * plain.FP32 * l.abs() + 2.0 ** -20).all()
+
+
+@pytest.mark.parametrize("G", [1, 2])
+@pytest.mark.parametrize("lens", [[0] * 40 + [5] + [0] * 70 + [300], [0] * 64, [1] * 32 + [0] * 32 + [129], [300] + [0] * 100])
+def test_windows_of_empty_sequences(dsa, lens, G):
+    T = sum(lens)
+    Q, K, V = make(2 * G, 2, max(T, 1), 64)
+    O, lse = torch.full_like(Q, 7.0), torch.full(Q.shape[:2], 9.0, device="cuda")
+    dsa.packed_prefill(Q, K, V, ints(cu_of(lens)), O=O, lse=lse)
+    assert dsa.device_status() == (0, 0)
+    assert T > 0 or (O == 7.0).all()
+    check(O, lse, Q, K, V, cu_of(lens))
