@@ -36,8 +36,8 @@ __device__ __forceinline__ int owner_of(const int* pre, int n, int i) {
 // search).  Nothing is read that the call writes: a taken page is looked up where it comes from, the old stack or the
 // row of the request that gave it back; pushes go behind the old stack, takes behind a row's old pages.  So no step
 // waits for another, but for one case: where lengths or count are updated in place, one cluster does all the work,
-// and its barrier stands between their reads and writes.  200K slots of 48 prompts: 4.7 us (17.3 as one cluster with
-// barriers between the steps); 256 requests of one token: 7 to 9 us.
+// and its barrier stands between their reads and writes.  197K slots of 48 prompts: 4.4 us apart, 17.5 in place (8 CTAs
+// write the slots); 256 requests of one token: 9.4 us either way.
 // ---------------------------------------------------------------------------
 constexpr int TAB_THREADS = 512;
 
@@ -389,16 +389,19 @@ __global__ void __launch_bounds__(ST_THREADS) k_cache_store(const __grid_constan
 // Attention of the newest n_q tokens of each request over its cached keys (itself among them):
 //   O = sum_j softmax_j(q . k_j ks / sqrt(d)) v_j vs,  j <= len - n_q + i for token i,
 // k, v: e4m3 values, ks, vs: their page's scales.
-// Bound by memory: 2 d bytes per key and KV head, read once.  All query heads of a KV head and all
-// n_q tokens are the columns of one n8 tile (or two), so each key is converted once; e4m3 is exact
-// in fp16, q is scaled by a power of two per row so that its 8 bits are exact in fp16 too, products
-// accumulate in fp32.  Keys (and, in the second product, value dimensions) are the m16 side of mma
+// Bound by memory: 2 d bytes per key and KV head, read once where a KV head has up to 16 rows (query heads
+// times n_q): they are the columns of one n8 tile (or two), so each key is converted once.  Each further 16
+// rows are a unit of their own and read the keys again.  32 requests of up to 8192 keys, 8 KV heads of d 128:
+// 51 us with 4 rows, 80 with 16, 137 with 32; 512 tokens of 4 heads behind 16384 keys 936 us.  e4m3 is exact
+// in fp16; q is scaled by a power of two per row so that its 8 bits are exact in fp16 too (elements under
+// 2^-30 of their row's largest are rounded, by at most 2^-38 of it); products accumulate in fp32.  Keys (and, in the second product, value dimensions) are the m16 side of mma
 // m16n8k16, S^T = K Q^T and O^T = V^T P^T: decoding has few queries, and as the m16 side they would
 // leave three quarters of the products and accumulators empty.  The tensor work is a fraction of what
 // the legacy path carries; tcgen05 would want 128 rows and both operands of 8 bits in one type.
 // Weights: with x = s ks and y = x + log2(vs) (log2 units), P = 2^(y - m + P_OFF) carries the value
 // scale, so pages of any scale share one accumulator, and l sums P / vs.  m lags the running
-// maximum by at most P_LAG: P <= 2^15 in fp16 (11 bits), underflow 2^-34 below the maximum.
+// maximum by at most P_LAG: P <= 2^15 in fp16, underflow 2^-34 below the maximum.  fp16 because it holds
+// e4m3 exactly and P to 11 bits, 8 times finer than the output's rounding.
 // Split: the work (64-key tiles of all requests, KV heads and row tiles, laid end to end) is
 // cut into equal ranges, one per CTA, a few CTAs per SM; so a long request spreads over many CTAs
 // and short ones share one.  A CTA's four warps take every fourth 16 keys, each through its own
@@ -411,7 +414,8 @@ constexpr int AT_WARPS = AT_THREADS / 32;
 constexpr int AT_KEYS = 16;                  // keys of a warp's step
 constexpr int AT_TILE = AT_KEYS * AT_WARPS;  // keys of a CTA's step
 constexpr int AT_MAX_CTAS = 592;             // sizes the workspace
-// A CTA takes at least so many tiles.  One request of 1000 tokens, 8 KV heads: 9.4 us with 4, 10.9 with 6, 12.4 with 8;
+// A CTA's range is at least so long, in tiles, with the start of a unit counted as AT_START of them; a range that lies in
+// a unit's start holds no key, and its CTA nothing to do.  One request of 1000 tokens, 8 KV heads: 9.4 us with 4, 10.9 with 6, 12.4 with 8;
 // one of 96396 tokens, 1 KV head, whose parts are many: 24, 21 and 20.
 constexpr int AT_MIN_TILES = 4;
 // A unit costs its tiles and this much for its start (pages, scales, Q): without it, CTAs whose range holds two units
@@ -420,7 +424,8 @@ constexpr int AT_MIN_TILES = 4;
 constexpr int AT_START = 4;
 constexpr float P_OFF = 10.f, P_LAG = 5.f;
 // CTAs of an SM, with at_stages() ring stages each: what counts is the bytes on their way.  d 128, a million keys of 8
-// heads: 352 us with 3 CTAs of 4 stages, 409 with 2 of 6, 422 with 4 of 3 (333 now, 98% of a copy's rate).  d 64 (boxes half as large), 20 requests
+// heads: 352 us with 3 CTAs of 4 stages, 409 with 2 of 6, 422 with 4 of 3 (336 now, 98% of a copy's rate; 367 to 389
+// after a tenth of a second of such calls, when the power cap has taken the SM clock from 1965 to some 1750 MHz).  d 64 (boxes half as large), 20 requests
 // of up to 4001 tokens, 16 heads: 37 us with 4 CTAs of 6 stages, 55 with 3 of 8.
 __host__ __device__ constexpr int at_per_sm(int d, int nq) { return d == 64 && nq == 1 ? 4 : 3; }
 __host__ __device__ constexpr int at_stages(int d) { return d == 128 ? 4 : 6; }
@@ -496,7 +501,7 @@ __device__ __forceinline__ uint32_t f16x2(float lo, float hi) {
   return *reinterpret_cast<const uint32_t*>(&v);
 }
 
-// Key tiles of request b; a length that its table row cannot hold is cut.
+// The length of request b; one that its table row cannot hold is cut.
 __device__ __forceinline__ int req_len(const AttendArgs& a, int b, bool tell) {
   const int l = a.lens[b];
   const int64_t most = (int64_t)a.width << a.shift;
@@ -1145,6 +1150,10 @@ dsa_status launch_attend(const dsa_cache& c, AttendArgs& a, cudaStream_t stream)
   cudaError_t e = serve_sms(&dev, &sms);
   if (e == cudaSuccess) e = serve_allow_smem<k_cache_attend<D, NQ>>(dev, AttendSmem<D>::bytes(MAX_REQ));
   const int smem = AttendSmem<D>::bytes(a.n_req);
+  // As many CTAs as an SM holds while the lengths in shared memory are short.  Above some 860 requests (d 64, one n8
+  // tile) or 1250 (d 128) fewer fit and the last ranges wait for the first; nothing depends on their running together.
+  // 32 query heads on 8, d 128, up to 300 keys each: 1024 requests 167 us (50 by their bytes), 4096 1226 us (201); the
+  // join, whose CTAs each sum all lengths, takes 37 and 334 of them.
   const int grid = min(at_per_sm(D, NQ) * sms, AT_MAX_CTAS);
   if (e == cudaSuccess) e = launch_pdl(k_cache_attend<D, NQ>, dim3(grid), dim3(AT_THREADS), (size_t)smem, stream, mk, mv, a);
   const int rows = min(16, a.n_q * a.G);

@@ -202,7 +202,8 @@ __device__ __forceinline__ void serve_add2(float& s0, float& s1, float a, float 
 }
 
 // (2^x0, 2^x1) on the multiply-add pipe, for x <= 100: 2^x = 2^n 2^f with n the nearest integer and a polynomial of
-// degree 5 in f (|f| <= 1/2, fitted for the smallest largest relative error, 7.5e-8; 2.1e-7 with its roundings).
+// degree 5 in f (|f| <= 1/2, fitted for a small largest relative error: 1.55e-7 with the coefficients below, 1.2e-7 at
+// f = 0; 2.1e-7 with its roundings).
 // Below -127 the result is 0, for -infinity too; NaN stays NaN.
 __device__ __forceinline__ void serve_ex2_poly2(float x0, float x1, float& p0, float& p1) {
   asm("max.NaN.f32 %0, %0, 0fC2FE0000;" : "+f"(x0));  // -127
