@@ -22,13 +22,20 @@ def _ptr(t):
     return ctypes.c_void_p(t.data_ptr()) if t is not None else ctypes.c_void_p(0)
 
 
-def _stream_ptr(stream, device):
-    """The handle of ``stream``, or of the current stream of ``device`` (the tensors')."""
-    if stream is None:
-        stream = torch.cuda.current_stream(device)
-    elif stream.device != device:
+# The handle of a device's current stream, and the current device: 0.1 us each, where
+# torch.cuda.current_stream takes 3 us.  A torch may lack them (one without CUDA does).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", lambda device: torch.cuda.current_stream(device).cuda_stream)
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+
+
+def _launch(device, stream, call, *args):
+    """call(*args, stream handle) on the tensors' device: on ``stream``, or on its current stream."""
+    if stream is not None and stream.device != device:
         raise ValueError(f"the stream belongs to {stream.device}, the tensors to {device}")
-    return ctypes.c_void_p(stream.cuda_stream)
+    if _current_device() != device.index:
+        with torch.cuda.device(device):
+            return _launch(device, stream, call, *args)
+    return call(*args, ctypes.c_void_p(_raw_stream(device.index) if stream is None else stream.cuda_stream))
 
 
 def make_problem(Q, K, V=None, O=None, block=64) -> B.dsa_problem:
@@ -172,9 +179,8 @@ def build_indices(Q, K, patterns, block, bufs: IndexBuffers | None = None, strea
     pats_c = patterns if isinstance(patterns, ctypes.Array) else make_patterns(patterns)
     if bufs is None:
         bufs = alloc_indices(prob, pats_c, Q.device)
-    with torch.cuda.device(Q.device):
-        st = B.dsa_build_indices(prob, _ptr(Q), _ptr(K), pats_c, bufs.c, _ptr(bufs.workspace),
-                                 bufs.workspace.numel(), _stream_ptr(stream, Q.device))
+    st = _launch(Q.device, stream, B.dsa_build_indices, prob, _ptr(Q), _ptr(K), pats_c, bufs.c, _ptr(bufs.workspace),
+                 bufs.workspace.numel())
     B.check(st, "dsa_build_indices")
     bufs._pats = pats_c
     return bufs
@@ -187,9 +193,7 @@ def sparse_prefill(Q, K, V, idx: IndexBuffers, O=None, lse=None, want_lse=False,
     if lse is None and want_lse:
         lse = torch.empty(Q.shape[0], Q.shape[1], dtype=torch.float32, device=Q.device)
     prob = make_problem(Q, K, V, O, block=idx.block)
-    with torch.cuda.device(Q.device):
-        st = B.dsa_sparse_prefill(prob, _ptr(Q), _ptr(K), _ptr(V), idx.c, _ptr(O), _ptr(lse),
-                                  _stream_ptr(stream, Q.device))
+    st = _launch(Q.device, stream, B.dsa_sparse_prefill, prob, _ptr(Q), _ptr(K), _ptr(V), idx.c, _ptr(O), _ptr(lse))
     B.check(st, "dsa_sparse_prefill")
     return O, lse
 
@@ -198,8 +202,7 @@ def count_pairs(Q, K, idx: IndexBuffers, stream=None) -> torch.Tensor:
     """Exact number of allowed (i, j) pairs per head (int64 tensor [Hq])."""
     pairs = torch.empty(Q.shape[0], dtype=torch.int64, device=Q.device)
     prob = make_problem(Q, K, block=idx.block)
-    with torch.cuda.device(Q.device):
-        B.check(B.dsa_count_pairs(prob, idx.c, _ptr(pairs), _stream_ptr(stream, Q.device)), "dsa_count_pairs")
+    B.check(_launch(Q.device, stream, B.dsa_count_pairs, prob, idx.c, _ptr(pairs)), "dsa_count_pairs")
     return pairs
 
 
@@ -208,8 +211,7 @@ def device_status(stream=None):
     stream); synchronises it."""
     if stream is None:
         stream = torch.cuda.current_stream()
-    with torch.cuda.device(stream.device):
-        return B.dsa_get_device_status(_stream_ptr(stream, stream.device))
+    return _launch(stream.device, stream, B.dsa_get_device_status)
 
 
 def indices_from_lists(heads, N, block, device="cuda") -> IndexBuffers:

@@ -18,16 +18,11 @@ from dataclasses import dataclass, field
 import torch
 
 from . import _binding as B
+from .api import _current_device, _raw_stream, build_indices, device_status, sparse_prefill
 
 
 def _refuse(what):
     raise ValueError(what)
-
-
-# The handle of a device's current stream, and the current device: 0.1 us each, where
-# torch.cuda.current_stream takes 3 us.  A torch may lack them (one without CUDA does).
-_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", lambda device: torch.cuda.current_stream(device).cuda_stream)
-_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
 @contextlib.contextmanager
@@ -79,12 +74,6 @@ def _apart(row, dims):
     return True
 
 
-def _output(O, heads, tokens, d, device):
-    _tokens("O", O, heads, tokens, d, device)
-    if O.numel() and not _apart(d, ((heads, O.stride(0)), (tokens, O.stride(1)))):
-        _refuse("O: rows must not overlap")
-
-
 def _rows(name, t, packed):
     """What the library asks of a tensor's rows: 16-byte pieces, and (packed) rows and heads apart."""
     if t.data_ptr() % 16:
@@ -122,10 +111,9 @@ def _lse(lse, want, shape, device):
 
 
 def _workspace(workspace, need, device):
-    if workspace is not None:
-        if (not isinstance(workspace, torch.Tensor) or workspace.device != device or not workspace.is_contiguous()
-                or workspace.nbytes < need or workspace.data_ptr() % 16):
-            _refuse(f"workspace must hold {need} bytes on {device}, from a multiple of 16 bytes on")
+    if (not isinstance(workspace, torch.Tensor) or workspace.device != device or not workspace.is_contiguous()
+            or workspace.nbytes < need or workspace.data_ptr() % 16):
+        _refuse(f"workspace must hold {need} bytes on {device}, from a multiple of 16 bytes on")
 
 
 def packed_prefill(Q, K, V, cu_seqlens, O=None, lse=None, want_lse=False, stream=None):
@@ -148,10 +136,17 @@ def packed_prefill(Q, K, V, cu_seqlens, O=None, lse=None, want_lse=False, stream
         _refuse("cu_seqlens must be an int32 tensor [sequences + 1]")
     _ints("cu_seqlens", cu_seqlens, cu_seqlens.shape, dev)
     if O is not None:
-        _output(O, Hq, T, d, dev)
+        _tokens("O", O, Hq, T, d, dev)
     if stream is not None or _current_device() != dev.index:
         with _elsewhere(dev, stream):
-            return packed_prefill(Q, K, V, cu_seqlens, O, lse, want_lse)
+            return _prefill(Q, K, V, cu_seqlens, O, lse, want_lse)
+    return _prefill(Q, K, V, cu_seqlens, O, lse, want_lse)
+
+
+# What runs behind a call's checks, on the current device and its current stream.
+def _prefill(Q, K, V, cu_seqlens, O=None, lse=None, want_lse=False):
+    Hq, T, d = Q.shape
+    Hkv, dev = K.shape[0], Q.device
     st = _raw_stream(dev.index)
     if O is None:
         O = torch.empty_like(Q, memory_format=torch.contiguous_format)
@@ -271,7 +266,12 @@ def build_tables(lens, new_lens, free_pages, free_count, block_table, page, max_
         _ints("out.free_count", out.free_count, (1,), dev)
     if stream is not None or _current_device() != dev.index:
         with _elsewhere(dev, stream):
-            return build_tables(lens, new_lens, free_pages, free_count, block_table, page, max_tokens, out, prompts)
+            return _build(lens, new_lens, free_pages, free_count, block_table, page, max_tokens, out, prompts)
+    return _build(lens, new_lens, free_pages, free_count, block_table, page, max_tokens, out, prompts)
+
+
+def _build(lens, new_lens, free_pages, free_count, block_table, page, max_tokens, out, prompts):
+    dev, (n, width) = lens.device, block_table.shape
     st = _raw_stream(dev.index)
     if out is None:
         new = torch.empty(max_tokens + 2 * n + 2, dtype=torch.int32, device=dev)
@@ -299,10 +299,13 @@ def cache_write(K, V, slots, cache, stream=None):
         return
     if stream is not None or _current_device() != dev.index:
         with _elsewhere(dev, stream):
-            return cache_write(K, V, slots, cache)
-    st = _raw_stream(dev.index)
-    B.check(B.lib().dsa_cache_write(ctypes.byref(c), K.data_ptr(), V.data_ptr(), *_strides(K), *_strides(V),
-                                    slots.data_ptr(), T, st), "dsa_cache_write")
+            return _write(K, V, slots, cache)
+    _write(K, V, slots, cache)
+
+
+def _write(K, V, slots, cache):
+    B.check(B.lib().dsa_cache_write(ctypes.byref(cache.c), K.data_ptr(), V.data_ptr(), *_strides(K), *_strides(V),
+                                    slots.data_ptr(), K.shape[1], _raw_stream(K.device.index)), "dsa_cache_write")
 
 
 def cache_attention(Q, cache, block_table, lens, n_q=1, O=None, lse=None, want_lse=False, workspace=None, stream=None):
@@ -325,18 +328,25 @@ def cache_attention(Q, cache, block_table, lens, n_q=1, O=None, lse=None, want_l
     if n_q < 1 or T != n * n_q:
         _refuse(f"Q has {T} rows, not {n_q} for each of {n} requests")
     if O is not None:
-        _output(O, Hq, T, d, dev)
-    need = B.lib().dsa_cache_attention_workspace(d)
-    _workspace(workspace, need, dev)
+        _tokens("O", O, Hq, T, d, dev)
+    if workspace is not None:
+        _workspace(workspace, B.lib().dsa_cache_attention_workspace(d), dev)
     if stream is not None or _current_device() != dev.index:
         with _elsewhere(dev, stream):
-            return cache_attention(Q, cache, block_table, lens, n_q, O, lse, want_lse, workspace)
+            return _attend(Q, cache, block_table, lens, n_q, O, lse, want_lse, workspace)
+    return _attend(Q, cache, block_table, lens, n_q, O, lse, want_lse, workspace)
+
+
+def _attend(Q, cache, block_table, lens, n_q, O=None, lse=None, want_lse=False, workspace=None):
+    c, dev = cache.c, cache.K.device
+    Hq, T, d = Q.shape
+    n, width = block_table.shape
     st = _raw_stream(dev.index)
     if O is None:
         O = torch.empty_like(Q, memory_format=torch.contiguous_format)
     lse = _lse(lse, want_lse, (Hq, T), dev)
     if workspace is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+        workspace = torch.empty(B.lib().dsa_cache_attention_workspace(d), dtype=torch.uint8, device=dev)
     if n > 0:
         B.check(B.lib().dsa_cache_attention(
             ctypes.byref(c), Q.data_ptr(), Hq, *_strides(Q), block_table.data_ptr(), width, lens.data_ptr(), n, n_q,
@@ -375,8 +385,11 @@ class PagedLayer:
         self.ones = torch.ones(requests, **ints)
 
     def _check(self, Q, K, V, packed):
-        """Refuses what a call behind build_tables would: by then tables and lengths have changed."""
+        """Refuses what a call behind build_tables would: by then tables and lengths have changed.  (What is checked here
+        is not checked there again.)"""
         c, dev = self.cache.c, self.cache.K.device
+        if self.lens.device != dev or self.lens.shape != (self.requests,):
+            _refuse(f"lens must stay an int32 tensor [{self.requests}] on {dev}")
         _tokens("Q", Q, self.Hq, None, c.d, dev)
         _tokens("K", K, c.Hkv, Q.shape[1] if packed else None, c.d, dev)
         _tokens("V", V, c.Hkv, K.shape[1], c.d, dev)
@@ -389,24 +402,28 @@ class PagedLayer:
         out = Tables(new[:T], new[T:], self.lens, self.free_count)
         build_tables(self.lens, new_lens, self.free_pages, self.free_count, self.table, self.page, T, out=out,
                      prompts=prompts)
-        cache_write(K, V, out.slots, self.cache)
+        if T > 0:
+            _write(K, V, out.slots, self.cache)
         return out
 
     def prefill(self, Q, K, V, new_lens, patterns=None, block=64):
-        """Prompts of requests that hold no tokens yet (each row sees the call's rows alone).  Q [Hq, T, d], K and V [Hkv, T, d] hold
-        their rows one after the other (T may be larger than their sum: the rows behind the last
-        are undefined in O), new_lens (int32 [requests]) says how many each gets: 0 for a request
-        that gets none, -1 for one that has ended and gives its pages back.  With ``patterns``
-        (as for ``build_indices``) all T rows are one request's prompt.  A request that gets tokens
-        though it holds some, or rows that are not one prompt's, are found on the GPU: nothing is
-        stored and ``status`` says DSA_ERR_DEVICE.  Returns O."""
+        """Prompts of requests that hold no tokens yet (each row sees the call's rows alone).  Q
+        [Hq, T, d], K and V [Hkv, T, d] hold their rows one after the other (T may be larger than
+        their sum: the rows behind the last are undefined in O), new_lens (int32 [requests]) says
+        how many each gets: 0 for a request that gets none, -1 for one that has ended and gives
+        its pages back.  With ``patterns`` (as for ``build_indices``) all T rows are one request's
+        prompt.  A request that gets tokens though it holds some, or rows that are not one
+        prompt's, are found on the GPU: nothing is stored and ``status`` says DSA_ERR_DEVICE.
+        Returns O."""
         self._check(Q, K, V, True)
         if not (0 if patterns is None else 1) <= Q.shape[1] <= 1 << 21:
             _refuse(f"a prefill takes up to {1 << 21} rows, not {Q.shape[1]}")
+        if _current_device() != self.lens.device.index:
+            with torch.cuda.device(self.lens.device):
+                return self.prefill(Q, K, V, new_lens, patterns, block)
         if patterns is None:
             out = self._store(K, V, new_lens, "packed")
-            return packed_prefill(Q, K, V, out.cu_seqlens)[0]
-        from .api import build_indices, sparse_prefill
+            return _prefill(Q, K, V, out.cu_seqlens)[0]
         _ints("new_lens", new_lens, (self.requests,), self.lens.device)
         O = sparse_prefill(Q, K, V, build_indices(Q, K, patterns, block))[0]  # first: it may refuse the patterns
         self._store(K, V, new_lens, "single")
@@ -428,11 +445,13 @@ class PagedLayer:
             if K.shape[1] < self.requests or (K.shape[1] > self.requests and n_q != 1):
                 _refuse(f"K has {K.shape[1]} rows; without new_lens each of {self.requests} requests gets one")
             new_lens = self.ones
+        if _current_device() != self.lens.device.index:
+            with torch.cuda.device(self.lens.device):
+                return self.decode(Q, K, V, new_lens, want_lse)
         self._store(K, V, new_lens)
-        return cache_attention(Q, self.cache, self.table, self.lens, n_q=n_q, want_lse=want_lse)
+        return _attend(Q, self.cache, self.table, self.lens, n_q, want_lse=want_lse)
 
     def status(self):
         """(status, detail) of the work on the current stream of the layer's device; synchronises it and clears the
         word."""
-        from .api import device_status
         return device_status(torch.cuda.current_stream(self.cache.K.device))

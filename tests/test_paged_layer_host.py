@@ -10,10 +10,12 @@ from dynamic_sparse_attention_build_b200 import serving
 def layer(monkeypatch):
     layer = dsa.PagedLayer.__new__(dsa.PagedLayer)
     layer.requests, layer.ones, layer.calls = 3, "ones", []
-    layer.cache = layer.table = layer.lens = None
+    layer.cache = layer.table = None
+    layer.lens = torch.zeros(3, dtype=torch.int32)
+    monkeypatch.setattr(serving, "_current_device", lambda: None)  # (as a host tensor's index)
     monkeypatch.setattr(layer, "_check", lambda *a: None)  # (the tensors are the host's)
     monkeypatch.setattr(layer, "_store", lambda K, V, new, **k: layer.calls.append((K.shape[1], new)))
-    monkeypatch.setattr(serving, "cache_attention", lambda Q, *a, n_q, **k: layer.calls.append(n_q))
+    monkeypatch.setattr(serving, "_attend", lambda Q, cache, table, lens, n_q, **k: layer.calls.append(n_q))
     return layer
 
 

@@ -241,5 +241,5 @@ def test_lse_and_workspace_that_are_no_tensors_are_refused():
     for bad in (1 << 20, [0] * 64, torch.zeros(15), torch.zeros(64)[::2], torch.zeros(65, dtype=torch.uint8)[1:]):
         with pytest.raises(ValueError, match="workspace"):
             serving._workspace(bad, 64, dev)
-    for good in (None, torch.zeros(16), torch.zeros(80, dtype=torch.uint8)):
+    for good in (torch.zeros(16), torch.zeros(80, dtype=torch.uint8)):
         serving._workspace(good, 64, dev)
