@@ -534,7 +534,7 @@ packed_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
         // than the weights' range bears, so there the product is rounded as m was.  (It stands where O is rescaled: in
         // a branch of its own it costs every half: 3 prompts of up to 4096 tokens, 16 heads of d 64, 107 us without, 110 here,
         // 121 there.)
-        const bool far = fabsf(m) >= 16777216.f;
+        const bool far = in && fabsf(m) >= 16777216.f;  // (rows behind the sequence may hold anything)
         const float scale = far ? 1.f : a.scale_log2;
         if (__any_sync(0xffffffffu, need || far)) {
           if (u > 0) {
