@@ -105,7 +105,8 @@ def _table(t):
 def _lse(lse, want, shape, device):
     if lse is None:
         return torch.empty(shape, dtype=torch.float32, device=device) if want else None
-    if not isinstance(lse, torch.Tensor) or lse.dtype is not torch.float32 or lse.device != device or lse.shape != shape or not lse.is_contiguous():
+    if (not isinstance(lse, torch.Tensor) or lse.dtype is not torch.float32 or lse.device != device or lse.shape != shape
+            or not lse.is_contiguous()):
         _refuse(f"lse must be a contiguous float32 tensor {tuple(shape)} on {device}")
     return lse
 
@@ -228,7 +229,7 @@ class Tables:
 PROMPTS = {None: (), "packed": (0,), "single": (1,)}
 
 
-def build_tables(lens, new_lens, free_pages, free_count, block_table, page, max_tokens, out=None, prompts=None, stream=None):
+def build_tables(lens, new_lens, free_pages, free_count, block_table, page, max_tokens, out=None, stream=None, prompts=None):
     """Pages and slots for the tokens that each request gets next; returns ``Tables``.
 
     lens, new_lens: int32 [B], the tokens that each request has and gets (a negative number

@@ -243,3 +243,15 @@ def test_lse_and_workspace_that_are_no_tensors_are_refused():
             serving._workspace(bad, 64, dev)
     for good in (torch.zeros(16), torch.zeros(80, dtype=torch.uint8)):
         serving._workspace(good, 64, dev)
+
+
+def test_serving_calls_keep_the_order_of_their_arguments():
+    """What a caller may pass by place; later arguments stand behind these."""
+    import inspect
+    import dynamic_sparse_attention_build_b200 as dsa
+    for call, names in ((dsa.build_tables, "lens new_lens free_pages free_count block_table page max_tokens out stream"),
+                        (dsa.packed_prefill, "Q K V cu_seqlens O lse want_lse stream"), (dsa.cache_write, "K V slots cache stream"),
+                        (dsa.cache_attention, "Q cache block_table lens n_q O lse want_lse workspace stream"),
+                        (dsa.build_indices, "Q K patterns block bufs stream"), (dsa.device_status, "stream"),
+                        (dsa.sparse_prefill, "Q K V idx O lse want_lse stream")):
+        assert list(inspect.signature(call).parameters)[:len(names.split())] == names.split()
