@@ -394,7 +394,8 @@ __global__ void __launch_bounds__(ST_THREADS) k_cache_store(const __grid_constan
 // rows are a unit of their own and read the keys again.  32 requests of up to 8192 keys, 8 KV heads of d 128:
 // 51 us with 4 rows, 80 with 16, 137 with 32; 512 tokens of 4 heads behind 16384 keys 936 us.  e4m3 is exact
 // in fp16; q is scaled by a power of two per row so that its 8 bits are exact in fp16 too (elements under
-// 2^-30 of their row's largest are rounded, by at most 2^-38 of it); products accumulate in fp32.  Keys (and, in the second product, value dimensions) are the m16 side of mma
+// 2^-30 of their row's largest are rounded, by at most 2^-38 of it); products accumulate in fp32.
+// Keys (and, in the second product, value dimensions) are the m16 side of mma
 // m16n8k16, S^T = K Q^T and O^T = V^T P^T: decoding has few queries, and as the m16 side they would
 // leave three quarters of the products and accumulators empty.  The tensor work is a fraction of what
 // the legacy path carries; tcgen05 would want 128 rows and both operands of 8 bits in one type.
@@ -415,8 +416,8 @@ constexpr int AT_KEYS = 16;                  // keys of a warp's step
 constexpr int AT_TILE = AT_KEYS * AT_WARPS;  // keys of a CTA's step
 constexpr int AT_MAX_CTAS = 592;             // sizes the workspace
 // A CTA's range is at least so long, in tiles, with the start of a unit counted as AT_START of them; a range that lies in
-// a unit's start holds no key, and its CTA nothing to do.  One request of 1000 tokens, 8 KV heads: 9.4 us with 4, 10.9 with 6, 12.4 with 8;
-// one of 96396 tokens, 1 KV head, whose parts are many: 24, 21 and 20.
+// a unit's start holds no key, and its CTA nothing to do.  One request of 1000 tokens, 8 KV heads: 9.4 us with 4, 10.9
+// with 6, 12.4 with 8; one of 96396 tokens, 1 KV head, whose parts are many: 24, 21 and 20.
 constexpr int AT_MIN_TILES = 4;
 // A unit costs its tiles and this much for its start (pages, scales, Q): without it, CTAs whose range holds two units
 // end last.  32 requests of up to 8192 keys, 8 heads of d 128: 58 us, 79 without; 10 of up to 4000, 16 heads of d 64:
@@ -425,8 +426,8 @@ constexpr int AT_START = 4;
 constexpr float P_OFF = 10.f, P_LAG = 5.f;
 // CTAs of an SM, with at_stages() ring stages each: what counts is the bytes on their way.  d 128, a million keys of 8
 // heads: 352 us with 3 CTAs of 4 stages, 409 with 2 of 6, 422 with 4 of 3 (336 now, 98% of a copy's rate; 367 to 389
-// after a tenth of a second of such calls, when the power cap has taken the SM clock from 1965 to some 1750 MHz).  d 64 (boxes half as large), 20 requests
-// of up to 4001 tokens, 16 heads: 37 us with 4 CTAs of 6 stages, 55 with 3 of 8.
+// after a tenth of a second of such calls, when the power cap has taken the SM clock from 1965 to some 1750 MHz).
+// d 64 (boxes half as large), 20 requests of up to 4001 tokens, 16 heads: 37 us with 4 CTAs of 6 stages, 55 with 3 of 8.
 __host__ __device__ constexpr int at_per_sm(int d, int nq) { return d == 64 && nq == 1 ? 4 : 3; }
 __host__ __device__ constexpr int at_stages(int d) { return d == 128 ? 4 : 6; }
 

@@ -4,9 +4,9 @@
 // query head h (KV head h / G, G = Hq / Hkv)
 //   O_i = sum_{j <= i, j in s} softmax_j(q_i.k_j / sqrt(d)) v_j,   lse_i = log sum_j exp(q_i.k_j / sqrt(d)).
 // One pass over the keys with a running maximum m and sum l per row; S and O accumulate in
-// fp32 (TMEM), l sums the unrounded P.  P is rounded to bf16 for the P.V product, the one type that
-// V's has in common with a P of any size (as in the sparse prefill): O is 1.9e-3 to 2.1e-3 from 64
-// bits, relative, where its own rounding alone makes 1.6e-3.
+// fp32 (TMEM), l sums the unrounded P.  P is rounded to bf16 for the P.V product, whose operands have one
+// type, V's (as in the sparse prefill): O is 1.9e-3 to 2.1e-3 from 64 bits, relative, where its own
+// rounding alone makes 1.6e-3.
 //
 // Design (persistent, one CTA per SM; an item = two 128-row query tiles that walk the same keys):
 //   * the two tiles are the same rows of two query heads of one KV head when G is even, else
@@ -531,9 +531,9 @@ packed_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
           m = m_new;
         }
         // s * scale - m in one rounding leaves what m's own rounding took, half a step of m: beyond 2^24 that is more
-        // than the weights' range bears, so there the product is rounded as m was.  (It stands where O is rescaled: in
-        // a branch of its own it costs every half: 3 prompts of up to 4096 tokens, 16 heads of d 64, 107 us without, 110 here,
-        // 121 there.)
+        // than the weights' range bears, so there the product is rounded as m was.  (It stands where O is rescaled; in
+        // a branch of its own it costs every half: 3 prompts of up to 4096 tokens, 16 heads of d 64, 121 us, 110 here,
+        // 107 without.)
         const bool far = in && fabsf(m) >= 16777216.f;  // (rows behind the sequence may hold anything)
         const float scale = far ? 1.f : a.scale_log2;
         if (__any_sync(0xffffffffu, need || far)) {
